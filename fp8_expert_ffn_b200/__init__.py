@@ -25,7 +25,15 @@ ENTRY_POINTS = ("moe_status_string", "moe_layer_create", "moe_layer_destroy", "m
                 "moe_kernels_per_forward", "moe_test_inject_stall", "moe_grouped_gate_up", "moe_grouped_down",
                 "moe_ep_pack_scales", "moe_ep_regroup", "moe_ep_unregroup", "moe_ep_comm_create",
                 "moe_ep_comm_export", "moe_ep_comm_connect", "moe_ep_comm_connect_local", "moe_ep_comm_buffers",
-                "moe_ep_comm_destroy", "moe_ep_plan", "moe_ep_dispatch", "moe_ep_combine")
+                "moe_ep_comm_destroy", "moe_ep_plan", "moe_ep_dispatch", "moe_ep_combine", "moe_grouped_mm",
+                "moe_grouped_mm_dgrad", "moe_grouped_mm_wgrad", "moe_swiglu", "moe_swiglu_backward",
+                "moe_w4_matvec", "moe_w4_gate_up")
+
+MOE_BF16, MOE_F16, MOE_F32 = range(3)   # moe_dtype
+
+# bits of the device status word (include/moe.h)
+MOE_STATUS_BAD_EXPERT, MOE_STATUS_DUP_EXPERT, MOE_STATUS_WAIT_TIMEOUT, MOE_STATUS_BAD_PLAN, MOE_STATUS_EP_OVERFLOW, \
+    MOE_STATUS_BOUNDS, MOE_STATUS_BAD_ROW = (1 << i for i in range(7))
 
 MOE_EP_HANDLE_BYTES = 64        # include/moe.h
 
@@ -50,6 +58,11 @@ class moe_weights(ctypes.Structure):
                 ("s_gate", ctypes.c_void_p), ("s_up", ctypes.c_void_p), ("s_down", ctypes.c_void_p),
                 ("router_w", ctypes.c_void_p), ("ld_h", ctypes.c_int), ("ld_f", ctypes.c_int),
                 ("router_bias", ctypes.c_void_p)]
+
+
+class moe_w4_weights(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+                ("scale_type", ctypes.c_int), ("group", ctypes.c_int), ("ld", ctypes.c_int)]
 
 
 _lib = None
@@ -100,6 +113,15 @@ def lib(build_if_missing: bool = True):
     L.moe_ep_plan.argtypes = [P, P, I, P, P, S, P]
     L.moe_ep_dispatch.argtypes = [P, P, P, I, I, P, P, P, P, P, S, P]
     L.moe_ep_combine.argtypes = [P, P, P, P, P, P, I, P, I, P]
+    Q = ctypes.c_longlong
+    W = ctypes.POINTER(moe_w4_weights)
+    for name in ("moe_grouped_mm", "moe_grouped_mm_dgrad"):
+        getattr(L, name).argtypes = [P, I, P, Q, P, Q, P, I, I, I, I, P, Q, P]
+    L.moe_grouped_mm_wgrad.argtypes = [P, I, P, Q, P, Q, P, I, I, I, I, P, Q, I, P]
+    L.moe_swiglu.argtypes = [P, I, P, Q, P, Q, P, I, I, P, Q, P]
+    L.moe_swiglu_backward.argtypes = [P, I, P, Q, P, Q, P, Q, P, I, I, P, Q, P, Q, P, Q, P]
+    L.moe_w4_matvec.argtypes = [P, I, P, I, Q, P, W, P, I, I, I, I, P, Q, P]
+    L.moe_w4_gate_up.argtypes = [P, I, P, I, Q, P, W, W, P, I, I, I, I, P, Q, P]
     for name in ENTRY_POINTS:
         if name not in ("moe_status_string", "moe_workspace_size"):
             getattr(L, name).restype = I
@@ -335,3 +357,66 @@ def moe_permute_noalloc(layer, x, T, ldx, topk_idx, offsets, perm, inv, xq, xs, 
     _check("moe_permute_noalloc",
            lib().moe_permute_noalloc(layer.handle, _ptr(x), T, ldx, _ptr(topk_idx), _ptr(offsets), _ptr(perm),
                                      _ptr(inv), _ptr(xq), _ptr(xs), _stream(stream)))
+
+
+def moe_grouped_mm(layer, type, x, ldx, w, ldw, offsets, rows, n, k, y_type, y, ldy, stream=None):
+    """y[r] = x[r] w[g]^T over the groups' rows; type, y_type: MOE_BF16, MOE_F16 (y also MOE_F32)."""
+    _check("moe_grouped_mm", lib().moe_grouped_mm(layer.handle, type, _ptr(x), ldx, _ptr(w), ldw, _ptr(offsets), rows,
+                                                  n, k, y_type, _ptr(y), ldy, _stream(stream)))
+
+
+def moe_grouped_mm_dgrad(layer, type, dy, lddy, w, ldw, offsets, rows, n, k, dx_type, dx, lddx, stream=None):
+    """dx[r] = dy[r] w[g]: the gradient of moe_grouped_mm for its rows."""
+    _check("moe_grouped_mm_dgrad",
+           lib().moe_grouped_mm_dgrad(layer.handle, type, _ptr(dy), lddy, _ptr(w), ldw, _ptr(offsets), rows, n, k,
+                                      dx_type, _ptr(dx), lddx, _stream(stream)))
+
+
+def moe_grouped_mm_wgrad(layer, type, dy, lddy, x, ldx, offsets, rows, n, k, dw_type, dw, lddw, accumulate=False,
+                         stream=None):
+    """dw[g] (+)= sum over g's rows of dy[r]^T x[r]: the gradient of moe_grouped_mm for its weights."""
+    _check("moe_grouped_mm_wgrad",
+           lib().moe_grouped_mm_wgrad(layer.handle, type, _ptr(dy), lddy, _ptr(x), ldx, _ptr(offsets), rows, n, k,
+                                      dw_type, _ptr(dw), lddw, int(bool(accumulate)), _stream(stream)))
+
+
+def moe_swiglu(layer, type, gate, ldg, up, ldu, offsets, rows, f, h, ldh, stream=None):
+    """h = silu(gate) * up over the groups' rows (offsets None: all rows)."""
+    _check("moe_swiglu", lib().moe_swiglu(layer.handle, type, _ptr(gate), ldg, _ptr(up), ldu, _ptr(offsets), rows, f,
+                                          _ptr(h), ldh, _stream(stream)))
+
+
+def moe_swiglu_backward(layer, type, dh, lddh, gate, ldg, up, ldu, offsets, rows, f, dgate, lddg, dup, lddu, h=None,
+                        ldh=0, stream=None):
+    """The gradient of moe_swiglu; h (optional): moe_swiglu's output again."""
+    _check("moe_swiglu_backward",
+           lib().moe_swiglu_backward(layer.handle, type, _ptr(dh), lddh, _ptr(gate), ldg, _ptr(up), ldu,
+                                     _ptr(offsets), rows, f, _ptr(dgate), lddg, _ptr(dup), lddu, _ptr(h), ldh,
+                                     _stream(stream)))
+
+
+class W4Weights:
+    """4-bit weights of a layer's experts (device tensors, kept alive): codes
+    [E+S][n][ld] uint8, scales [E+S][n][ceil(k/group)] of scale_type, zeros
+    uint8 of the scales' shape or None (8 everywhere)."""
+
+    def __init__(self, codes, scales, zeros, scale_type, group, ld=None):
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+        self.desc = moe_w4_weights(_ptr(codes), _ptr(scales), _ptr(zeros), scale_type, group,
+                                   codes.shape[-1] if ld is None else ld)
+
+
+def moe_w4_matvec(layer, type, x, x_rows, ldx, perm, w: W4Weights, offsets, rows, n, k, y_type, y, ldy, stream=None):
+    """y[r] = x[perm[r]] w[g]^T with 4-bit weights (perm None: x[r])."""
+    _check("moe_w4_matvec",
+           lib().moe_w4_matvec(layer.handle, type, _ptr(x), x_rows, ldx, _ptr(perm), ctypes.byref(w.desc),
+                               _ptr(offsets), rows, n, k, y_type, _ptr(y), ldy, _stream(stream)))
+
+
+def moe_w4_gate_up(layer, type, x, x_rows, ldx, perm, gate: W4Weights, up: W4Weights, offsets, rows, f, k, h_type, h,
+                   ldh, stream=None):
+    """h[r] = silu(x[perm[r]] gate[g]^T) * (x[perm[r]] up[g]^T) with 4-bit weights."""
+    _check("moe_w4_gate_up",
+           lib().moe_w4_gate_up(layer.handle, type, _ptr(x), x_rows, ldx, _ptr(perm), ctypes.byref(gate.desc),
+                                ctypes.byref(up.desc), _ptr(offsets), rows, f, k, h_type, _ptr(h), ldh,
+                                _stream(stream)))

@@ -75,6 +75,34 @@ bool encode_tmap_u8(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t 
   return encode_tmap(tm, false, base, inner, rows, depth, ld, depth_stride);
 }
 
+bool encode_tmap_16(CUtensorMap* tm, moe_dtype t, const void* base, uint64_t inner, uint64_t rows, uint64_t depth,
+                    uint64_t ld, uint32_t box_inner, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {inner, rows, depth};
+  cuuint64_t strides[2] = {ld * 2, rows * ld * 2};
+  cuuint32_t box[3] = {box_inner, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(tm, t == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  depth ? 3u : 2u, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool encode_tmap_codes(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t rows, uint64_t depth, uint64_t ld,
+                       uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {inner, rows, depth};
+  cuuint64_t strides[2] = {ld, rows * ld};
+  cuuint32_t box[3] = {64, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 Scratch carve(const moe_layer_s* L, int T, void* base) {
   Scratch s = {};
   const int K = L->K, E = L->E;
@@ -134,6 +162,8 @@ moe_status check_ws(const moe_layer_s* L, int T, void* ws, size_t ws_bytes) {
 }
 
 constexpr int kMaxT = 1 << 20;
+constexpr int kMaxDim = 1 << 16;          // weight rows and columns of the 16-bit and 4-bit operators
+constexpr long long kMaxLd = 1ll << 20;   // their row strides (an expert's bytes stay below the tensor maps' 2^40)
 
 }  // namespace
 
@@ -448,6 +478,161 @@ moe_status moe_test_grouped_gemm_f32(moe_layer_t L, int which, const uint8_t* a,
   if (!a || !as || !offsets || !out) return MOE_ERR_INVALID_ARG;
   if (!aligned16(a)) return MOE_ERR_MISALIGNED;
   return from_cuda(launch_test_gemm_f32(L, which, a, as, offsets, T, out, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// Expert operators beside the FP8 layer: 16-bit grouped products and their
+// gradients, SwiGLU and its gradient, 4-bit products. They take the handle
+// for its groups, device and status word, so a routing-only handle will do.
+
+static bool is_type16(moe_dtype t) { return t == MOE_BF16 || t == MOE_F16; }
+static bool is_type(moe_dtype t) { return is_type16(t) || t == MOE_F32; }
+
+// The handle's device has to be the current one: the stream is taken there.
+static moe_status check_op(moe_layer_t L, int rows) {
+  if (!L || rows < 0 || rows > kMaxT * 9) return MOE_ERR_INVALID_ARG;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  if (dev != L->device) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+static moe_status check_mm(moe_layer_t L, moe_dtype t, const void* a, long long lda, int ca, const void* b,
+                           long long ldb, int cb, const int32_t* offsets, int rows, int n, int k, moe_dtype out_t,
+                           const void* out, long long ldo, int co) {
+  if (!is_type16(t) || !(out_t == t || out_t == MOE_F32)) return MOE_ERR_INVALID_ARG;
+  if (n < 1 || k < 1 || n > kMaxDim || k > kMaxDim || lda < ca || ldb < cb || ldo < co || lda > kMaxLd ||
+      ldb > kMaxLd || ldo > kMaxLd)
+    return MOE_ERR_INVALID_ARG;
+  if (!offsets || !out || !a || !b) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(b) || lda % 8 != 0 || ldb % 8 != 0) return MOE_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(out) % (out_t == MOE_F32 ? 4 : 2) != 0) return MOE_ERR_MISALIGNED;
+  return check_op(L, rows);
+}
+
+moe_status moe_grouped_mm(moe_layer_t L, moe_dtype t, const void* x, long long ldx, const void* w, long long ldw,
+                          const int32_t* offsets, int rows, int n, int k, moe_dtype y_type, void* y, long long ldy,
+                          void* stream) {
+  if (!L || rows < 0) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  moe_status s = check_mm(L, t, x, ldx, k, w, ldw, k, offsets, rows, n, k, y_type, y, ldy, n);
+  if (s != MOE_OK) return s;
+  return from_cuda(launch_grouped_mm(L, MOE_MM_FORWARD, t, x, ldx, w, ldw, offsets, rows, n, k, y_type, y, ldy, 0,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_grouped_mm_dgrad(moe_layer_t L, moe_dtype t, const void* dy, long long lddy, const void* w,
+                                long long ldw, const int32_t* offsets, int rows, int n, int k, moe_dtype dx_type,
+                                void* dx, long long lddx, void* stream) {
+  if (!L || rows < 0) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  moe_status s = check_mm(L, t, dy, lddy, n, w, ldw, k, offsets, rows, n, k, dx_type, dx, lddx, k);
+  if (s != MOE_OK) return s;
+  return from_cuda(launch_grouped_mm(L, MOE_MM_DGRAD, t, dy, lddy, w, ldw, offsets, rows, n, k, dx_type, dx, lddx, 0,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_grouped_mm_wgrad(moe_layer_t L, moe_dtype t, const void* dy, long long lddy, const void* x,
+                                long long ldx, const int32_t* offsets, int rows, int n, int k, moe_dtype dw_type,
+                                void* dw, long long lddw, int accumulate, void* stream) {
+  if (!L || rows < 0 || (accumulate != 0 && accumulate != 1)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) {   // every group is empty: the gradient is zero, whatever the operands are
+    if (!is_type16(t) || !(dw_type == t || dw_type == MOE_F32) || !dw || n < 1 || k < 1 || n > kMaxDim ||
+        k > kMaxDim || lddw < k || lddw > kMaxLd)
+      return MOE_ERR_INVALID_ARG;
+    const size_t es = dw_type == MOE_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(dw) % es != 0) return MOE_ERR_MISALIGNED;
+    moe_status s = check_op(L, rows);
+    if (s != MOE_OK || accumulate) return s;
+    return from_cuda(cudaMemset2DAsync(dw, size_t(lddw) * es, 0, size_t(k) * es, size_t(L->E + L->S) * n,
+                                       static_cast<cudaStream_t>(stream)));
+  }
+  moe_status s = check_mm(L, t, dy, lddy, n, x, ldx, k, offsets, rows, n, k, dw_type, dw, lddw, k);
+  if (s != MOE_OK) return s;
+  return from_cuda(launch_grouped_mm(L, MOE_MM_WGRAD, t, dy, lddy, x, ldx, offsets, rows, n, k, dw_type, dw, lddw,
+                                     accumulate, static_cast<cudaStream_t>(stream)));
+}
+
+static moe_status check_act(moe_dtype t, int f, const void* const* p, const long long* ld, int count) {
+  if (!is_type(t) || f < 1 || f > kMaxDim) return MOE_ERR_INVALID_ARG;
+  for (int i = 0; i < count; ++i) {
+    if (!p[i] || ld[i] < f || ld[i] > kMaxLd) return MOE_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(p[i]) % (t == MOE_F32 ? 4 : 2) != 0) return MOE_ERR_MISALIGNED;
+  }
+  return MOE_OK;
+}
+
+moe_status moe_swiglu(moe_layer_t L, moe_dtype t, const void* gate, long long ldg, const void* up, long long ldu,
+                      const int32_t* offsets, int rows, int f, void* h, long long ldh, void* stream) {
+  if (!L || rows < 0) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  const void* p[] = {gate, up, h};
+  const long long ld[] = {ldg, ldu, ldh};
+  moe_status s = check_act(t, f, p, ld, 3);
+  if (s == MOE_OK) s = check_op(L, rows);
+  if (s != MOE_OK) return s;
+  return from_cuda(launch_swiglu(L, t, gate, ldg, up, ldu, offsets, rows, f, h, ldh, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_swiglu_backward(moe_layer_t L, moe_dtype t, const void* dh, long long lddh, const void* gate,
+                               long long ldg, const void* up, long long ldu, const int32_t* offsets, int rows, int f,
+                               void* dgate, long long lddg, void* dup, long long lddu, void* h, long long ldh,
+                               void* stream) {
+  if (!L || rows < 0) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  const void* p[] = {dh, gate, up, dgate, dup, h};
+  const long long ld[] = {lddh, ldg, ldu, lddg, lddu, ldh};
+  moe_status s = check_act(t, f, p, ld, h ? 6 : 5);
+  if (s == MOE_OK && (dgate == dup || (h && (h == dgate || h == dup)))) s = MOE_ERR_INVALID_ARG;
+  if (s == MOE_OK) s = check_op(L, rows);
+  if (s != MOE_OK) return s;
+  return from_cuda(launch_swiglu_backward(L, t, dh, lddh, gate, ldg, up, ldu, offsets, rows, f, dgate, lddg, dup, lddu,
+                                          h, ldh, static_cast<cudaStream_t>(stream)));
+}
+
+static moe_status check_w4(const moe_w4_weights* w, int k) {
+  if (!w || !w->codes || !w->scales || !is_type(w->scale_type)) return MOE_ERR_INVALID_ARG;
+  if (w->group != 32 && w->group != 64 && w->group != 128) return MOE_ERR_INVALID_ARG;
+  if (w->ld < (k + 1) / 2 || w->ld > kMaxDim) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w->codes) || w->ld % 16 != 0) return MOE_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(w->scales) % (w->scale_type == MOE_F32 ? 4 : 2) != 0) return MOE_ERR_MISALIGNED;
+  return MOE_OK;
+}
+
+static moe_status w4_call(moe_layer_t L, moe_dtype t, const void* x, int x_rows, long long ldx, const int32_t* perm,
+                          const moe_w4_weights* w, const moe_w4_weights* up, bool dual, const int32_t* offsets,
+                          int rows, int n, int k, moe_dtype y_t, void* y, long long ldy, void* stream) {
+  if (!L || rows < 0) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!is_type16(t) || !(y_t == t || y_t == MOE_F32)) return MOE_ERR_INVALID_ARG;
+  if (n < 1 || k < 1 || n > kMaxDim || k > kMaxDim || ldx < k || ldx > kMaxLd || ldy < n || ldy > kMaxLd ||
+      x_rows < 1 || x_rows > kMaxT * 9 || !x || !y || !offsets || (!perm && x_rows < rows))
+    return MOE_ERR_INVALID_ARG;
+  moe_status s = check_w4(w, k);
+  if (s == MOE_OK && dual) {
+    s = check_w4(up, k);
+    if (s == MOE_OK && (w->group != up->group || w->scale_type != up->scale_type || w->ld != up->ld ||
+                        (w->zeros == nullptr) != (up->zeros == nullptr)))
+      s = MOE_ERR_INVALID_ARG;
+  }
+  if (s != MOE_OK) return s;
+  if (!aligned16(x) || ldx % 8 != 0) return MOE_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(y) % (y_t == MOE_F32 ? 4 : 2) != 0) return MOE_ERR_MISALIGNED;
+  if ((s = check_op(L, rows)) != MOE_OK) return s;
+  return from_cuda(launch_w4(L, t, x, x_rows, ldx, perm, w, dual ? up : nullptr, offsets, rows, n, k, y_t, y, ldy,
+                             static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_w4_matvec(moe_layer_t L, moe_dtype t, const void* x, int x_rows, long long ldx, const int32_t* perm,
+                         const moe_w4_weights* w, const int32_t* offsets, int rows, int n, int k, moe_dtype y_t,
+                         void* y, long long ldy, void* stream) {
+  return w4_call(L, t, x, x_rows, ldx, perm, w, nullptr, false, offsets, rows, n, k, y_t, y, ldy, stream);
+}
+
+moe_status moe_w4_gate_up(moe_layer_t L, moe_dtype t, const void* x, int x_rows, long long ldx, const int32_t* perm,
+                          const moe_w4_weights* gate, const moe_w4_weights* up, const int32_t* offsets, int rows,
+                          int f, int k, moe_dtype h_t, void* h, long long ldh, void* stream) {
+  return w4_call(L, t, x, x_rows, ldx, perm, gate, up, true, offsets, rows, f, k, h_t, h, ldh, stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -1,0 +1,470 @@
+// Products grouped by expert over ragged rows, in bf16 or fp16 with fp32
+// accumulation: the forward product of an expert's weight and its two
+// gradients. With group g's rows r in [offsets[g], offsets[g+1]):
+//   forward  y[r, n]     = sum_k x[r, k] w[g, n, k]
+//   dgrad    dx[r, k]    = sum_n dy[r, n] w[g, n, k]
+//   wgrad    dw[g, n, k] = sum_r dy[r, n] x[r, k]   (+ dw when accumulating)
+//
+// All three are one tile product D[c, r] = sum_i A[i, c] B[i, r]: c is the
+// output's contiguous dimension, r its rows, i the contraction. The output's
+// columns sit on the MMA's M dimension (TMEM lanes) and its rows on N, so
+//   - a ragged group costs only the MMA columns of its own rows (N is the
+//     number of rows rounded up to 32, 256 at most) where rows on M would
+//     always pay for 128 or 256;
+//   - rows past the group's end are other columns of D that are never
+//     stored: whatever they hold (NaN included) cannot reach a result.
+// The operands are read as they lie in memory: forward, both K-major; dgrad,
+// A = w with the contraction n as its slow dimension (MN-major); wgrad, both
+// MN-major over the group's rows. A wgrad block that passes the group's end
+// has the rows past it set to zero in shared memory before the MMA (both
+// operands, so that a NaN there is not multiplied by zero).
+//
+// Kernel layout: CTA pairs (cluster of 2, tcgen05 cta_group::2, M 256 x N up
+// to 256 x K 16 per instruction), persistent over a device-side tile list.
+// Each CTA holds its own 128 columns of A and half of B's rows, so a
+// 256 x 256 tile moves 32 KB per CTA and 64-deep K block from L2 where two
+// independent 128 x 256 tiles would move 48 KB.
+//   warp 0      TMA producer into a 6-stage ring (16 KB of A, up to 16 KB of B)
+//   warp 1      TMEM allocation; in the leading CTA the MMA issuer
+//   warp 2      relay: waits for its CTA's copies, zeroes a wgrad tail, and
+//               signals the leading CTA
+//   warp 3      idle
+//   warps 4-7   epilogue: TMEM lanes 32*(w%4).., one output column per lane;
+//               two 256-column TMEM buffers overlap it with the next tile
+// No TMA multicast; commits signal both CTAs. Every wait is bounded (1 s): on
+// a timeout the status word is set, all roles leave, copies in flight are
+// waited for (bounded) and the TMEM is released.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "groups.cuh"
+#include "internal.h"
+#include "pair.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int BC = 256;                 // output columns per tile (128 per CTA)
+constexpr int BR = 256;                 // output rows per tile, at most
+constexpr int BK = 64;                  // contraction per stage (128 bytes)
+constexpr int STAGES = 6;
+constexpr int A_BYTES = 128 * BK * 2;   // 16 KB
+constexpr int B_BYTES = 128 * BK * 2;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int BOX_BYTES = 64 * 64 * 2;  // one MN-major box: 64 contraction rows x 64 columns
+constexpr int THREADS = 256;
+constexpr int FIRST_EPI_WARP = 4;
+constexpr int EPI_WARPS = 4;
+constexpr int RCHUNK = 8;               // row tiles per chunk of the tile order
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int SMEM_DYN = STAGES * STAGE_BYTES + 1024;
+
+struct GmmArgs {
+  const int32_t* offsets;   // [ngroups + 1]
+  int ngroups, nweights;    // groups of the offsets; groups that have weights
+  int rows;                 // rows of the row operands
+  int nr, nc;               // wgrad: output rows (n) per group; all: output columns
+  int ntc;                  // column tiles
+  int nk;                   // forward, dgrad: K blocks of a tile
+  void* out;
+  long long ld;             // output row stride, elements
+  int out_type;             // moe_dtype
+  int accumulate;           // wgrad: add to what `out` holds
+  uint32_t idesc;           // instruction descriptor without N
+  uint32_t* status;
+  unsigned long long wait_ns;
+  int withhold;             // test only: the first CTA's producer skips its first stage
+};
+
+// Tensor maps of the row operand K-major: boxes of 128, 64, 32 and 16 rows,
+// so that a tile of few rows moves few bytes.
+struct RowMaps {
+  CUtensorMap m[4];
+};
+
+struct Tile {
+  int g, col0, row0, nrows, r_first, nk;
+  // row0: first output row (global for forward/dgrad, within the group's
+  // weight for wgrad); nrows: valid rows; r_first, wgrad: the group's first row
+};
+
+template <int MODE>
+__device__ __forceinline__ Tile decode_tile(int i, const GroupPlan& s, const GmmArgs& p) {
+  Tile t;
+  t.g = find_group(s.prefix, p.ngroups, i);
+  const int local = i - s.prefix[t.g];
+  const int g0 = s.off[t.g], n_g = s.off[t.g + 1] - g0;
+  if (MODE == MOE_MM_WGRAD) {
+    const int rt = local / p.ntc;
+    t.col0 = (local - rt * p.ntc) * BC;
+    t.row0 = rt * BR;
+    t.nrows = min(BR, p.nr - t.row0);
+    t.r_first = g0;
+    t.nk = (n_g + BK - 1) / BK;
+  } else {
+    // chunks of up to 8 row tiles, then the column tiles, then the row tiles:
+    // the row tiles that share a weight tile run side by side
+    const int rts = (n_g + BR - 1) / BR;
+    const int per_chunk = RCHUNK * p.ntc;
+    const int chunk = local / per_chunk;
+    const int within = local - chunk * per_chunk;
+    const int rc = min(RCHUNK, rts - chunk * RCHUNK);
+    const int ct = within / rc;
+    const int rt = chunk * RCHUNK + (within - ct * rc);
+    t.col0 = ct * BC;
+    t.row0 = g0 + rt * BR;
+    t.nrows = min(BR, n_g - rt * BR);
+    t.r_first = 0;
+    t.nk = p.nk;
+  }
+  return t;
+}
+
+// MMA columns of a tile: its rows rounded up to 32 (each CTA holds half).
+__device__ __forceinline__ int tile_n(const Tile& t) { return (t.nrows + 31) & ~31; }
+
+// Stores a lane's 32 (or the first m) output rows of one column, from `at`
+// on; one rounding, to nearest even, of the fp32 sum.
+template <typename T>
+__device__ __forceinline__ float load_as_f32(const T* o);
+template <>
+__device__ __forceinline__ float load_as_f32<float>(const float* o) { return *o; }
+template <>
+__device__ __forceinline__ float load_as_f32<__nv_bfloat16>(const __nv_bfloat16* o) { return __bfloat162float(*o); }
+template <>
+__device__ __forceinline__ float load_as_f32<__half>(const __half* o) { return __half2float(*o); }
+__device__ __forceinline__ void store_f32(float* o, float v) { *o = v; }
+__device__ __forceinline__ void store_f32(__nv_bfloat16* o, float v) { *o = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store_f32(__half* o, float v) { *o = __float2half_rn(v); }
+
+template <typename T>
+__device__ __forceinline__ void store_rows(T* o, long long ld, const float (&v)[32], int m, int accumulate) {
+  if (accumulate) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < m) store_f32(o + j * ld, load_as_f32(o + j * ld) + v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < m) store_f32(o + j * ld, v[j]);
+  }
+}
+
+__device__ __forceinline__ void store_chunk(const GmmArgs& p, size_t at, const float (&v)[32], int m) {
+  if (p.out_type == MOE_F32)
+    store_rows(static_cast<float*>(p.out) + at, p.ld, v, m, p.accumulate);
+  else if (p.out_type == MOE_BF16)
+    store_rows(static_cast<__nv_bfloat16*>(p.out) + at, p.ld, v, m, p.accumulate);
+  else
+    store_rows(static_cast<__half*>(p.out) + at, p.ld, v, m, p.accumulate);
+}
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    grouped_mm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ RowMaps tmB, const GmmArgs p) {
+  constexpr bool A_MN = MODE != MOE_MM_FORWARD;   // A's contraction is its slow dimension
+  constexpr bool B_MN = MODE == MOE_MM_WGRAD;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[STAGES];    // this CTA's copies of a stage
+  __shared__ __align__(8) uint64_t ready_bar[STAGES];   // leading CTA: both CTAs' stages complete
+  __shared__ __align__(8) uint64_t empty_bar[STAGES];
+  __shared__ __align__(8) uint64_t tfull_bar[2];
+  __shared__ __align__(8) uint64_t tempty_bar[2];       // leading CTA: both CTAs' epilogues
+  __shared__ __align__(8) uint64_t done_bar;
+  __shared__ GroupPlan s_plan;
+  __shared__ uint32_t tmem_base_s;
+  __shared__ int s_abort_store;
+  __shared__ uint32_t s_relayed;
+  volatile int* s_abort = &s_abort_store;
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&ready_bar[s], 2);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull_bar[b], 1);
+      mbar_init(&tempty_bar[b], 2 * EPI_WARPS);
+    }
+    mbar_init(&done_bar, 1);
+    s_abort_store = 0;
+    s_relayed = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    for (int j = 0; j < (B_MN ? 1 : 4); ++j) tma_prefetch_desc(&tmB.m[j]);
+  }
+  if (warp == 1) tmem_alloc_pair(&tmem_base_s, TMEM_COLS);
+  // the set-up above overlaps the previous kernel; offsets, operands and
+  // outputs are touched only below
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const int total = build_plan<THREADS>(
+      s_plan, p.offsets, p.ngroups, p.nweights, p.rows, p.status, [&](int n_g) -> int {
+        if (MODE == MOE_MM_WGRAD) return ((p.nr + BR - 1) / BR) * p.ntc;
+        return ((n_g + BR - 1) / BR) * p.ntc;
+      });
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the peer's barriers are initialised and its TMEM is allocated
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_base_s;
+  uint32_t issued = 0;
+  uint32_t withheld = 0xFFFFFFFFu;
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- producer
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int i = pair; ok && i < total; i += npairs) {
+        const Tile t = decode_tile<MODE>(i, s_plan, p);
+        const int half = tile_n(t) >> 1;
+        const int acol = t.col0 + int(rank) * 128;
+        const int brow = t.row0 + int(rank) * half;
+        const uint32_t bytes = A_BYTES + (B_MN ? ((half + 63) >> 6) * BOX_BYTES : half * BK * 2);
+        for (int kb = 0; kb < t.nk; ++kb) {
+          const int s = it % STAGES;
+          if (!mbar_wait(&empty_bar[s], ((it / STAGES) & 1u) ^ 1u, s_abort, p.status, p.wait_ns)) { ok = false; break; }
+          if (p.withhold && blockIdx.x == 0 && it == 0) {   // test only: this stage never arrives
+            withheld = it++;
+            continue;
+          }
+          uint8_t* a = smem + s * STAGE_BYTES;
+          uint8_t* b = a + A_BYTES;
+          const int k0 = (MODE == MOE_MM_WGRAD ? t.r_first : 0) + kb * BK;
+          mbar_arrive_expect_tx(&full_bar[s], bytes);
+          if (MODE == MOE_MM_FORWARD) {
+            tma_load_3d(a, &tmA, &full_bar[s], k0, acol, t.g);
+          } else if (MODE == MOE_MM_DGRAD) {
+            tma_load_3d(a, &tmA, &full_bar[s], acol, k0, t.g);
+            tma_load_3d(a + BOX_BYTES, &tmA, &full_bar[s], acol + 64, k0, t.g);
+          } else {
+            tma_load_2d(a, &tmA, &full_bar[s], acol, k0);
+            tma_load_2d(a + BOX_BYTES, &tmA, &full_bar[s], acol + 64, k0);
+          }
+          if (B_MN) {
+            for (int c = 0; c < half; c += 64) tma_load_2d(b + c * (BK * 2), &tmB.m[0], &full_bar[s], brow + c, k0);
+          } else {
+            int r = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {   // 128, 64, 32, 16 rows: half is a multiple of 16, 128 at most
+              const int h = 128 >> j;
+              if (half & h) {
+                tma_load_2d(b + r * (BK * 2), &tmB.m[j], &full_bar[s], k0, brow + r);
+                r += h;
+              }
+            }
+          }
+          ++it;
+        }
+      }
+      issued = it;
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (rank == 0 && lane == 0) {
+      uint32_t it = 0, tb = 0;
+      bool ok = true;
+      for (int i = pair; ok && i < total; i += npairs) {
+        const Tile t = decode_tile<MODE>(i, s_plan, p);
+        if (t.nk == 0) continue;
+        const uint32_t idesc = p.idesc | (uint32_t(tile_n(t) >> 3) << 17);
+        const uint32_t buf = tb & 1u;
+        if (!mbar_wait_cluster(&tempty_bar[buf], ((tb >> 1) & 1u) ^ 1u, s_abort, p.status, p.wait_ns)) break;
+        const uint32_t d = tmem_base + buf * BR;
+        for (int kb = 0; kb < t.nk; ++kb) {
+          const int s = it % STAGES;
+          if (!mbar_wait_cluster(&ready_bar[s], (it / STAGES) & 1u, s_abort, p.status, p.wait_ns)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(smem + s * STAGE_BYTES);
+          const uint64_t ad = A_MN ? smem_desc_mn_sw128(a_addr, BOX_BYTES) : smem_desc_sw128(a_addr);
+          const uint64_t bd = B_MN ? smem_desc_mn_sw128(a_addr + A_BYTES, BOX_BYTES) : smem_desc_sw128(a_addr + A_BYTES);
+#pragma unroll
+          for (int k = 0; k < BK / 16; ++k)
+            // 16 of the contraction: 32 bytes along a K-major row, two 8-row
+            // atoms (2048 bytes) of an MN-major box (address field in 16 bytes)
+            mma_f16_pair(d, ad + uint64_t(k * (A_MN ? 128 : 2)), bd + uint64_t(k * (B_MN ? 128 : 2)), idesc,
+                         (kb | k) ? 1u : 0u);
+          tc_commit_pair(&empty_bar[s]);
+          ++it;
+        }
+        if (!ok) break;
+        tc_commit_pair(&tfull_bar[buf]);
+        ++tb;
+      }
+      tc_commit_pair_self(&done_bar);   // all MMAs issued above have completed
+      int never = 0;
+      mbar_wait(&done_bar, 0, &never, p.status, p.wait_ns);
+    }
+  } else if (warp == 2) {
+    // ----------------------------------------------------------------- relay
+    uint32_t it = 0;
+    bool ok = true;
+    for (int i = pair; ok && i < total; i += npairs) {
+      const Tile t = decode_tile<MODE>(i, s_plan, p);
+      int left = 0;   // wgrad: the group's rows from the current block on
+      if (MODE == MOE_MM_WGRAD) left = s_plan.off[t.g + 1] - t.r_first;
+      for (int kb = 0; kb < t.nk; ++kb) {
+        const int s = it % STAGES;
+        const bool got = mbar_wait(&full_bar[s], (it / STAGES) & 1u, s_abort, p.status, p.wait_ns);
+        if (!__all_sync(0xFFFFFFFFu, got)) { ok = false; break; }
+        if (MODE == MOE_MM_WGRAD) {
+          if (left < BK) {
+            // rows [left, 64) of every box belong to the next group (or lie
+            // past the last row): set them to zero
+            const int boxes = 2 + ((tile_n(t) / 2 + 63) >> 6);
+            const int vecs = (BK - left) * 8;   // 16-byte pieces per box
+            for (int v = lane; v < boxes * vecs; v += 32) {
+              const int bx = v / vecs;
+              *reinterpret_cast<uint4*>(smem + s * STAGE_BYTES + bx * BOX_BYTES + left * 128 + (v - bx * vecs) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          left -= BK;
+        }
+        if (lane == 0) mbar_arrive_rank(&ready_bar[s], 0);
+        ++it;
+      }
+    }
+    if (lane == 0) s_relayed = it;
+  } else if (warp >= FIRST_EPI_WARP) {
+    // -------------------------------------------------------------- epilogue
+    const int q = warp & 3;   // TMEM lane quarter this warp may access
+    uint32_t tb = 0;
+    for (int i = pair; i < total; i += npairs) {
+      const Tile t = decode_tile<MODE>(i, s_plan, p);
+      const int col = t.col0 + int(rank) * 128 + q * 32 + lane;
+      const bool cv = col < p.nc;
+      size_t at = size_t(t.row0) * size_t(p.ld) + size_t(col);
+      if (MODE == MOE_MM_WGRAD) at += size_t(t.g) * size_t(p.nr) * size_t(p.ld);
+      if (t.nk == 0) {   // wgrad of a group without rows
+        if (!p.accumulate && cv) {
+          float z[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z[j] = 0.0f;
+          for (int c = 0; c < t.nrows; c += 32) store_chunk(p, at + size_t(c) * size_t(p.ld), z, min(32, t.nrows - c));
+        }
+        continue;
+      }
+      const uint32_t buf = tb & 1u;
+      const bool got = mbar_wait(&tfull_bar[buf], (tb >> 1) & 1u, s_abort, p.status, p.wait_ns);
+      if (!__all_sync(0xFFFFFFFFu, got)) break;
+      tc_fence_after();
+      const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + buf * BR;
+      for (int c = 0; c < t.nrows; c += 32) {
+        float v[32];
+        tmem_ld32(tbase + uint32_t(c), v);
+        tmem_ld_wait();
+        if (c + 32 >= t.nrows) {   // the buffer is in registers: hand it back
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_rank(&tempty_bar[buf], 0);
+        }
+        if (cv) store_chunk(p, at + size_t(c) * size_t(p.ld), v, min(32, t.nrows - c));
+      }
+      ++tb;
+    }
+  }
+  // ------------------------------------------------------------------ teardown
+  __syncthreads();
+  if (warp == 0 && lane == 0) {
+    // copies issued but never relayed (only after an abort) must land first
+    int never = 0;
+    for (uint32_t j = s_relayed; j < issued; ++j)
+      if (j != withheld) mbar_wait(&full_bar[j % STAGES], (j / STAGES) & 1u, &never, p.status, p.wait_ns);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs are past their last remote arrival and MMA
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+  cluster_sync();
+}
+
+template <int MODE>
+cudaError_t launch_mode(const moe_layer_s* L, const CUtensorMap& tmA, const RowMaps& tmB, GmmArgs a, long long tiles,
+                        cudaStream_t st) {
+  static std::atomic<bool> configured[kMaxDevices];   // the attribute is per device
+  cudaError_t ce = once_per_device(configured, []() {
+    return cudaFuncSetAttribute(grouped_mm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_DYN);
+  });
+  if (ce != cudaSuccess) return ce;
+  a.wait_ns = kWaitLimitNs;
+  if (L->test_stall_ns) {   // a test armed a stall for this one launch
+    a.wait_ns = L->test_stall_ns;
+    a.withhold = 1;
+    L->test_stall_ns = 0;
+  }
+  const long long pairs = tiles < L->num_sms / 2 ? tiles : L->num_sms / 2;
+  if (pairs <= 0) return cudaSuccess;
+  return launch_pdl(grouped_mm_kernel<MODE>, dim3(unsigned(2 * pairs)), dim3(THREADS), SMEM_DYN, st, tmA, tmB, a);
+}
+
+// A row operand [rows][cols] whose rows are the tile's N (K-major boxes).
+bool encode_row_maps(RowMaps* m, moe_dtype t, const void* base, int cols, int rows, long long ld) {
+  for (int j = 0; j < 4; ++j)
+    if (!encode_tmap_16(&m->m[j], t, base, cols, rows, 0, ld, 64, 128u >> j)) return false;
+  return true;
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_mm(const moe_layer_s* L, int mode, moe_dtype t, const void* a, long long lda, const void* b,
+                              long long ldb, const int32_t* offsets, int rows, int n, int k, moe_dtype out_t, void* out,
+                              long long ldo, int accumulate, cudaStream_t st) {
+  const int G = L->E + L->S;
+  GmmArgs p = {};
+  p.offsets = offsets;
+  p.ngroups = L->E + 1;
+  p.nweights = G;
+  p.rows = rows;
+  p.out = out;
+  p.ld = ldo;
+  p.out_type = out_t;
+  p.accumulate = accumulate;
+  p.status = L->status;
+  p.idesc = idesc_16(t, 256, mode != MOE_MM_FORWARD, mode == MOE_MM_WGRAD);
+  CUtensorMap tmA;
+  RowMaps tmB;
+  if (mode == MOE_MM_WGRAD) {
+    // a = dy [rows][n], b = x [rows][k]; output rows n, columns k
+    p.nr = n;
+    p.nc = k;
+    p.ntc = (k + BC - 1) / BC;
+    if (!encode_tmap_16(&tmA, t, b, k, rows, 0, ldb, 64, 64) || !encode_tmap_16(&tmB.m[0], t, a, n, rows, 0, lda, 64, 64))
+      return cudaErrorInvalidValue;
+    for (int j = 1; j < 4; ++j) tmB.m[j] = tmB.m[0];
+    return launch_mode<MOE_MM_WGRAD>(L, tmA, tmB, p, static_cast<long long>(G) * ((n + BR - 1) / BR) * p.ntc, st);
+  }
+  // a = the rows, b = w [G][n][k]
+  const int contraction = mode == MOE_MM_FORWARD ? k : n;
+  p.nc = mode == MOE_MM_FORWARD ? n : k;
+  p.ntc = (p.nc + BC - 1) / BC;
+  p.nk = (contraction + BK - 1) / BK;
+  if (!encode_tmap_16(&tmA, t, b, k, n, G, ldb, 64, mode == MOE_MM_FORWARD ? 128 : 64) ||
+      !encode_row_maps(&tmB, t, a, contraction, rows, lda))
+    return cudaErrorInvalidValue;
+  // upper bound on the tiles: every group may add one partial row tile
+  const long long tiles = (static_cast<long long>(rows) / BR + (rows < G ? rows : G)) * p.ntc;
+  if (mode == MOE_MM_FORWARD) return launch_mode<MOE_MM_FORWARD>(L, tmA, tmB, p, tiles, st);
+  return launch_mode<MOE_MM_DGRAD>(L, tmA, tmB, p, tiles, st);
+}
+
+}  // namespace moe

@@ -1,0 +1,76 @@
+// The group plan that every expert operator derives on the device from the
+// offsets of its launch: checked offsets in shared memory and the exclusive
+// prefix of a per-group work count.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+constexpr int kMaxGroups = 257;   // 256 routed experts and the shared one
+
+struct GroupPlan {
+  int off[kMaxGroups + 1];     // row offsets, [ngroups + 1]
+  int prefix[kMaxGroups + 1];  // exclusive prefix of the work counts
+  int wsum[32];
+};
+
+// Fills `s` from offsets[0..ngroups] with count(rows of the group) units of
+// work per group; returns the total, or -1 when the offsets start below 0,
+// decrease, end beyond `rows`, or give rows to a group without weights
+// (index >= nweights): the launch then does no work and has set
+// STATUS_BAD_PLAN. Called by all THREADS threads of the block, which take
+// the groups in rounds; ends with a block barrier.
+template <int THREADS, typename F>
+__device__ __forceinline__ int build_plan(GroupPlan& s, const int32_t* __restrict__ offsets, int ngroups, int nweights,
+                                          int rows, uint32_t* status, F count) {
+  int base = 0;
+  int bad_any = 0;
+  for (int g0 = 0; g0 < ngroups; g0 += THREADS) {
+    const int g = g0 + int(threadIdx.x);
+    int v = 0, bad = 0;
+    if (g < ngroups) {
+      const int o0 = offsets[g], o1 = offsets[g + 1];
+      bad = o0 < 0 || o1 < o0 || o1 > rows || (g >= nweights && o1 != o0);
+      s.off[g] = o0;
+      if (g == ngroups - 1) s.off[ngroups] = o1;
+      if (!bad && g < nweights) v = count(o1 - o0);
+    }
+    int incl = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if ((threadIdx.x & 31) >= d) incl += o;
+    }
+    if ((threadIdx.x & 31) == 31) s.wsum[threadIdx.x >> 5] = incl;
+    bad_any |= __syncthreads_or(bad);
+    int before = base, all = base;
+    for (int j = 0; j < THREADS / 32; ++j) {
+      const int w = s.wsum[j];
+      if (j < int(threadIdx.x >> 5)) before += w;
+      all += w;
+    }
+    if (g < ngroups) s.prefix[g] = before + incl - v;
+    if (g == ngroups - 1) s.prefix[ngroups] = before + incl;
+    base = all;
+    __syncthreads();   // wsum is rewritten in the next round; prefix and off are complete
+  }
+  if (bad_any) {
+    if (threadIdx.x == 0) set_status(status, STATUS_BAD_PLAN);
+    return -1;
+  }
+  return base;
+}
+
+// The group that holds unit i of the work list (groups without units are
+// passed over): the last one whose prefix is <= i.
+__device__ __forceinline__ int find_group(const int* prefix, int ngroups, int i) {
+  int lo = 0, hi = ngroups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] <= i) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+}  // namespace moe

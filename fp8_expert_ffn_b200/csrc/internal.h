@@ -183,6 +183,34 @@ bool encode_tmap_u8(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t 
 // Same for bf16 (box 64 x 128 elements = 128 bytes of K per row) or u8.
 bool encode_tmap(CUtensorMap* tm, bool bf16, const void* base, uint64_t inner, uint64_t rows, uint64_t depth,
                  uint64_t ld_bytes, uint64_t depth_stride_bytes, bool force3d = false, uint32_t box_rows = 128);
+// Map of a 16-bit matrix [depth][rows][inner] (depth 0: 2-D) with row stride
+// `ld` elements (groups rows * ld apart), boxes of box_rows x box_inner
+// elements, 128-byte swizzle; elements past the extents read as zero.
+bool encode_tmap_16(CUtensorMap* tm, moe_dtype t, const void* base, uint64_t inner, uint64_t rows, uint64_t depth,
+                    uint64_t ld, uint32_t box_inner, uint32_t box_rows);
+// Map of 4-bit codes [depth][rows][inner bytes], row stride `ld` bytes, boxes
+// of box_rows x 64 bytes with 64-byte swizzle.
+bool encode_tmap_codes(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t rows, uint64_t depth, uint64_t ld,
+                       uint32_t box_rows);
+// Products grouped by expert in 16-bit types (gmm.cu). forward and dgrad:
+// a = the row operand, b = the weights; wgrad: a = dy, b = x.
+enum { MOE_MM_FORWARD = 0, MOE_MM_DGRAD = 1, MOE_MM_WGRAD = 2 };
+cudaError_t launch_grouped_mm(const moe_layer_s* L, int mode, moe_dtype t, const void* a, long long lda, const void* b,
+                              long long ldb, const int32_t* offsets, int rows, int n, int k, moe_dtype out_t, void* out,
+                              long long ldo, int accumulate, cudaStream_t st);
+// SwiGLU over grouped rows and its gradient (swiglu.cu).
+cudaError_t launch_swiglu(const moe_layer_s* L, moe_dtype t, const void* gate, long long ldg, const void* up,
+                          long long ldu, const int32_t* offsets, int rows, int f, void* h, long long ldh,
+                          cudaStream_t st);
+cudaError_t launch_swiglu_backward(const moe_layer_s* L, moe_dtype t, const void* dh, long long lddh, const void* gate,
+                                   long long ldg, const void* up, long long ldu, const int32_t* offsets, int rows,
+                                   int f, void* dgate, long long lddg, void* dup, long long lddu, void* h,
+                                   long long ldh, cudaStream_t st);
+// Products with 4-bit weights for few rows per expert (w4.cu); up = null:
+// the plain product, else h = silu(gate) * up.
+cudaError_t launch_w4(const moe_layer_s* L, moe_dtype t, const void* x, int x_rows, long long ldx, const int32_t* perm,
+                      const moe_w4_weights* w, const moe_w4_weights* up, const int32_t* offsets, int rows, int n,
+                      int k, moe_dtype out_t, void* y, long long ldy, cudaStream_t st);
 // Experts per router tile (the router weight map's box height).
 constexpr uint32_t kRouterExperts = 128;
 

@@ -406,6 +406,127 @@ moe_status moe_ep_combine(moe_layer_t route_layer, moe_ep_comm_t comm, const int
 moe_status moe_combine(moe_layer_t layer, const uint16_t* y, const int32_t* inv, const float* topk_w, int T,
                        uint16_t* out, int ldo, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Expert operators beside the FP8 layer: the same experts in 16-bit weights
+ * (served, or trained: products and gradients) and in 4-bit weights (decode).
+ * Conventions on top of those above:
+ *   - `layer` gives the groups (E = n_routed, S = n_shared), the device and
+ *     the status word; a routing-only handle is enough. Its hidden and ffn
+ *     are not used: the sizes are arguments. The current device must be the
+ *     handle's, else MOE_ERR_INVALID_ARG;
+ *   - offsets [E+2] are the groups' rows as moe_permute, moe_ep_plan or
+ *     moe_ep_dispatch write them: group g is rows [offsets[g], offsets[g+1]),
+ *     empty groups are allowed, group E must be empty when S = 0. Rows before
+ *     offsets[0] and from offsets[E+1] to `rows` belong to no group: what
+ *     they hold is not used and their outputs are left as they were. Offsets
+ *     that start below 0, decrease or end beyond `rows` set
+ *     MOE_STATUS_BAD_PLAN and nothing is written;
+ *   - element types are named by moe_dtype; sums are held in fp32 and each
+ *     output is rounded once, to nearest even;
+ *   - NaN and infinities follow IEEE arithmetic and stay in the rows (for
+ *     weight gradients: in the groups) that they belong to;
+ *   - 1 <= n, k, f <= 65536, row strides at most 2^20 elements, `rows` at
+ *     most 9 * 2^20; rows = 0 is a no-op (a weight gradient is still set);
+ *   - inputs and outputs must not overlap unless a call says so;
+ *   - nothing is allocated and no workspace is used, so calls on different
+ *     streams may overlap. */
+typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype;
+
+/* Products grouped by expert over ragged rows: the gate, up and down
+ * projections of the model's BF16 checkpoint (model card
+ * dots-studio/dots3-note-prev, "Model Overview": BF16 and FP8; SwiGLU experts
+ * without biases), with their two gradients for training. With w[g] the
+ * [n][k] weight of group g (rows ldw elements apart, groups n * ldw):
+ *   moe_grouped_mm        y[r]  = x[r] w[g]^T                 x [rows][ldx], y [rows][ldy]
+ *   moe_grouped_mm_dgrad  dx[r] = dy[r] w[g]                  dy [rows][lddy], dx [rows][lddx]
+ *   moe_grouped_mm_wgrad  dw[g] = sum over g's rows of dy[r]^T x[r], [E+S][n][lddw],
+ *                         plus what dw holds when accumulate = 1; a group
+ *                         without rows gets zero (or is left, accumulating)
+ *   type     MOE_BF16 or MOE_F16: x, dy and w
+ *   *_type   the output's: `type` or MOE_F32
+ *   x, dy, w 16-byte aligned with strides that are multiples of 8 elements;
+ *            outputs may have any stride and need their element's alignment
+ * Each output's sum has a fixed order: results do not change from run to
+ * run, nor with the other rows of the batch. */
+moe_status moe_grouped_mm(moe_layer_t layer, moe_dtype type, const void* x, long long ldx, const void* w,
+                          long long ldw, const int32_t* offsets, int rows, int n, int k, moe_dtype y_type, void* y,
+                          long long ldy, void* stream);
+/* Gradient of moe_grouped_mm for its rows, as described there. Training: no
+ * counterpart on the pages. */
+moe_status moe_grouped_mm_dgrad(moe_layer_t layer, moe_dtype type, const void* dy, long long lddy, const void* w,
+                                long long ldw, const int32_t* offsets, int rows, int n, int k, moe_dtype dx_type,
+                                void* dx, long long lddx, void* stream);
+/* Gradient of moe_grouped_mm for its weights, as described there. Training:
+ * no counterpart on the pages. */
+moe_status moe_grouped_mm_wgrad(moe_layer_t layer, moe_dtype type, const void* dy, long long lddy, const void* x,
+                                long long ldx, const int32_t* offsets, int rows, int n, int k, moe_dtype dw_type,
+                                void* dw, long long lddw, int accumulate, void* stream);
+
+/* SwiGLU between the products (Dots3NoteTextConfig: hidden_act silu):
+ *   h[r, j] = silu(gate[r, j]) * up[r, j],  silu(g) = g / (1 + exp(-g))
+ * over the rows of all groups (offsets as above; NULL: all `rows` rows).
+ *   type   MOE_BF16, MOE_F16 or MOE_F32: gate, up [rows][ld] and h; fp32
+ *          arithmetic; any stride, aligned to the element. h may be gate or
+ *          up itself (same pointer and stride). */
+moe_status moe_swiglu(moe_layer_t layer, moe_dtype type, const void* gate, long long ldg, const void* up,
+                      long long ldu, const int32_t* offsets, int rows, int f, void* h, long long ldh, void* stream);
+/* Gradient of moe_swiglu, with s = 1 / (1 + exp(-gate)):
+ *   dup = dh * gate * s,   dgate = dh * up * s * (1 + gate * (1 - s))
+ * and, when h is not NULL, h itself again (so that training keeps gate and up
+ * only; its bits are moe_swiglu's). dgate, dup and h may each be one of the
+ * inputs (same pointer and stride), but not one another. Training: no
+ * counterpart on the pages. */
+moe_status moe_swiglu_backward(moe_layer_t layer, moe_dtype type, const void* dh, long long lddh, const void* gate,
+                               long long ldg, const void* up, long long ldu, const int32_t* offsets, int rows, int f,
+                               void* dgate, long long lddg, void* dup, long long lddu, void* h, long long ldh,
+                               void* stream);
+
+/* 4-bit expert weights: w[g][j][i] = (code - zero) * scale, with one scale
+ * (and zero point) per `group` consecutive columns of a row.
+ *   codes   [E+S][n][ld] bytes: column 2i in the low half of byte i, column
+ *           2i+1 in the high half; ld a multiple of 16, at least
+ *           ceil(k/2), at most 65536; 16-byte aligned
+ *   scales  [E+S][n][ceil(k/group)] of scale_type (any moe_dtype)
+ *   zeros   the same shape, bytes 0..15 (only the low 4 bits are used), or
+ *           NULL: 8 everywhere
+ *   group   32, 64 or 128 (the last group of a row may be short)
+ * Rows and groups are contiguous (n and k are the call's). */
+typedef struct {
+  const uint8_t* codes;
+  const void* scales;
+  const uint8_t* zeros;
+  moe_dtype scale_type;
+  int group;
+  int ld;
+} moe_w4_weights;
+
+/* Matrix-vector products with 4-bit expert weights, for decode batches: the
+ * weights of every group that has rows are streamed once per 16 of its rows,
+ * so it is meant for a few rows per expert (it is right for any number).
+ *   y[r] = x[perm[r]] w[g]^T   (perm NULL: x[r])
+ *   x     [x_rows][ldx] of `type` (MOE_BF16 or MOE_F16), 16-byte aligned,
+ *         ldx a multiple of 8; perm [rows] as moe_permute writes it: one
+ *         token's x serves all its experts without a copy. A row whose perm
+ *         lies outside [0, x_rows) reads as zero and sets
+ *         MOE_STATUS_BAD_ROW; without perm x_rows must be at least rows
+ *   y     [rows][ldy] of y_type (`type` or MOE_F32), any stride
+ * Codes less zero points are exact in `type`; products are summed in fp32
+ * per group of columns and the scale is applied to that sum in fp32. The
+ * order of every sum is fixed. The pages describe no such call. */
+moe_status moe_w4_matvec(moe_layer_t layer, moe_dtype type, const void* x, int x_rows, long long ldx,
+                         const int32_t* perm, const moe_w4_weights* w, const int32_t* offsets, int rows, int n, int k,
+                         moe_dtype y_type, void* y, long long ldy, void* stream);
+/* The gate and up products of a SwiGLU expert with 4-bit weights and the
+ * activation, in one kernel: h[r] = silu(x wg^T) * (x wu^T), both products
+ * and the activation in fp32 (they are not rounded in between), h [rows][ldh]
+ * of h_type. gate and up are both [E+S][f][k] with the same group,
+ * scale_type and ld, and both or neither have zeros; the rest as at
+ * moe_w4_matvec. The pages describe no such call. */
+moe_status moe_w4_gate_up(moe_layer_t layer, moe_dtype type, const void* x, int x_rows, long long ldx,
+                          const int32_t* perm, const moe_w4_weights* gate, const moe_w4_weights* up,
+                          const int32_t* offsets, int rows, int f, int k, moe_dtype h_type, void* h, long long ldh,
+                          void* stream);
+
 /* The whole MoE layer of the dots3-note language model (Dots3NoteTextConfig;
  * model card dots-studio/dots3-note-prev, "Model Overview": 256 routed + 1
  * shared experts, top-8):
@@ -423,6 +544,7 @@ moe_status moe_layer_forward(moe_layer_t layer, const uint16_t* x, int T, int ld
 #define MOE_STATUS_BOUNDS 0x20u      /* bounds-checked build only: a row index taken from the inputs
                                       (inv, offsets, segment counts) fell outside its buffer; the
                                       access was skipped */
+#define MOE_STATUS_BAD_ROW 0x40u     /* a row's perm lies outside the rows of x; it was read as zero */
 
 /* Synchronises `stream`, returns MOE_ERR_DEVICE if any kernel of this layer
  * flagged an error since the last call (and clears the flag), else MOE_OK.
