@@ -176,7 +176,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   __shared__ GroupPlan s_plan;
   __shared__ uint32_t tmem_base_s;
   __shared__ int s_abort_store;
-  __shared__ uint32_t s_relayed;
+  __shared__ uint32_t s_relayed, s_issued, s_withheld;
   volatile int* s_abort = &s_abort_store;
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -197,6 +197,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     mbar_init(&done_bar, 1);
     s_abort_store = 0;
     s_relayed = 0;
+    s_issued = 0;
+    s_withheld = 0xFFFFFFFFu;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
@@ -220,12 +222,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync();   // the peer's barriers are initialised and its TMEM is allocated
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_s;
-  uint32_t issued = 0;
-  uint32_t withheld = 0xFFFFFFFFu;
 
   if (warp == 0) {
     // -------------------------------------------------------------- producer
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t it = 0;
       bool ok = true;
       for (int i = pair; ok && i < total; i += npairs) {
@@ -236,9 +236,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const uint32_t bytes = A_BYTES + (B_MN ? ((half + 63) >> 6) * BOX_BYTES : half * BK * 2);
         for (int kb = 0; kb < t.nk; ++kb) {
           const int s = it % STAGES;
-          if (!mbar_wait(&empty_bar[s], ((it / STAGES) & 1u) ^ 1u, s_abort, p.status, p.wait_ns)) { ok = false; break; }
+          if (!mbar_wait_stage(&empty_bar[s], ((it / STAGES) & 1u) ^ 1u, s_abort, p.status, p.wait_ns)) { ok = false; break; }
           if (p.withhold && blockIdx.x == 0 && it == 0) {   // test only: this stage never arrives
-            withheld = it++;
+            s_withheld = it++;
             continue;
           }
           uint8_t* a = smem + s * STAGE_BYTES;
@@ -270,11 +270,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           ++it;
         }
       }
-      issued = it;
+      s_issued = it;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (rank == 0 && lane == 0) {
+    if (rank == 0 && elect_one()) {
       uint32_t it = 0, tb = 0;
       bool ok = true;
       for (int i = pair; ok && i < total; i += npairs) {
@@ -282,11 +282,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (t.nk == 0) continue;
         const uint32_t idesc = p.idesc | (uint32_t(tile_n(t) >> 3) << 17);
         const uint32_t buf = tb & 1u;
-        if (!mbar_wait_cluster(&tempty_bar[buf], ((tb >> 1) & 1u) ^ 1u, s_abort, p.status, p.wait_ns)) break;
+        if (!mbar_wait_stage(&tempty_bar[buf], ((tb >> 1) & 1u) ^ 1u, s_abort, p.status, p.wait_ns)) break;
         const uint32_t d = tmem_base + buf * BR;
         for (int kb = 0; kb < t.nk; ++kb) {
           const int s = it % STAGES;
-          if (!mbar_wait_cluster(&ready_bar[s], (it / STAGES) & 1u, s_abort, p.status, p.wait_ns)) { ok = false; break; }
+          if (!mbar_wait_stage(&ready_bar[s], (it / STAGES) & 1u, s_abort, p.status, p.wait_ns)) { ok = false; break; }
+          if (MODE == MOE_MM_WGRAD && kb == t.nk - 1) cluster_fence();   // the relays' zeros
           tc_fence_after();
           const uint32_t a_addr = smem_u32(smem + s * STAGE_BYTES);
           const uint64_t ad = A_MN ? smem_desc_mn_sw128(a_addr, BOX_BYTES) : smem_desc_sw128(a_addr);
@@ -306,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       tc_commit_pair_self(&done_bar);   // all MMAs issued above have completed
       int never = 0;
-      mbar_wait(&done_bar, 0, &never, p.status, p.wait_ns);
+      mbar_wait_stage(&done_bar, 0, &never, p.status, p.wait_ns);
     }
   } else if (warp == 2) {
     // ----------------------------------------------------------------- relay
@@ -318,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (MODE == MOE_MM_WGRAD) left = s_plan.off[t.g + 1] - t.r_first;
       for (int kb = 0; kb < t.nk; ++kb) {
         const int s = it % STAGES;
-        const bool got = mbar_wait(&full_bar[s], (it / STAGES) & 1u, s_abort, p.status, p.wait_ns);
+        const bool got = mbar_wait_stage(&full_bar[s], (it / STAGES) & 1u, s_abort, p.status, p.wait_ns);
         if (!__all_sync(0xFFFFFFFFu, got)) { ok = false; break; }
         if (MODE == MOE_MM_WGRAD) {
           if (left < BK) {
@@ -333,6 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             }
             fence_proxy_async_smem();
             __syncwarp();
+            cluster_fence();   // the leading CTA's MMAs read these zeros
           }
           left -= BK;
         }
@@ -361,7 +363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         continue;
       }
       const uint32_t buf = tb & 1u;
-      const bool got = mbar_wait(&tfull_bar[buf], (tb >> 1) & 1u, s_abort, p.status, p.wait_ns);
+      const bool got = mbar_wait_stage(&tfull_bar[buf], (tb >> 1) & 1u, s_abort, p.status, p.wait_ns);
       if (!__all_sync(0xFFFFFFFFu, got)) break;
       tc_fence_after();
       const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + buf * BR;
@@ -384,8 +386,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (warp == 0 && lane == 0) {
     // copies issued but never relayed (only after an abort) must land first
     int never = 0;
-    for (uint32_t j = s_relayed; j < issued; ++j)
-      if (j != withheld) mbar_wait(&full_bar[j % STAGES], (j / STAGES) & 1u, &never, p.status, p.wait_ns);
+    for (uint32_t j = s_relayed; j < s_issued; ++j)
+      if (j != s_withheld) mbar_wait_stage(&full_bar[j % STAGES], (j / STAGES) & 1u, &never, p.status, p.wait_ns);
   }
   tc_fence_before();
   __syncthreads();

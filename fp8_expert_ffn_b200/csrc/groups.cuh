@@ -9,6 +9,29 @@ namespace moe {
 
 constexpr int kMaxGroups = 257;   // 256 routed experts and the shared one
 
+// mbar_wait that reads the clock only now and then: the expert operators'
+// roles wait on every stage, often for a fraction of a microsecond, which one
+// read of the global timer already takes. Same limit, abort flag and status.
+__device__ __forceinline__ bool mbar_wait_stage(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status,
+                                                unsigned long long limit_ns) {
+  const uint32_t a = smem_u32(bar);
+  unsigned long long t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(a, parity)) return true;
+    if ((i & 31u) == 0) {
+      if (*abort) return false;
+      const unsigned long long now = globaltimer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > limit_ns) {
+        set_status(status, STATUS_WAIT_TIMEOUT);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
 struct GroupPlan {
   int off[kMaxGroups + 1];     // row offsets, [ngroups + 1]
   int prefix[kMaxGroups + 1];  // exclusive prefix of the work counts

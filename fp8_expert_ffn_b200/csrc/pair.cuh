@@ -15,52 +15,40 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 
+// True in one lane of a converged warp. The compiler knows the branch it
+// guards to hold one thread, so the copies and MMAs in it take their operands
+// from uniform registers; behind `lane == 0` each issue cost 250 cycles.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Barrier over all threads of the cluster (orders shared-memory accesses).
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// Arrives once on the barrier at the same address in CTA `rank` of the cluster.
+// Arrives once on the barrier at the same address in CTA `rank` of the
+// cluster. The arrival orders what hardware units wrote (copies and MMAs that
+// this thread has waited for); a thread's own stores to shared memory that
+// the other CTA's MMAs are to see need cluster_fence on both sides. (With
+// .release.cluster and .acquire.cluster on every stage instead, the two
+// fences cost a microsecond per stage.)
 __device__ __forceinline__ void mbar_arrive_rank(uint64_t* bar, uint32_t rank) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\t"
       "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)),
+      "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)),
       "r"(rank)
       : "memory");
 }
 
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar_addr, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar_addr), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// mbar_wait for a barrier that threads of the peer CTA arrive on (acquires at
-// cluster scope); same limit, abort flag and status.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                                  uint32_t* status, unsigned long long limit_ns) {
-  const uint32_t a = smem_u32(bar);
-  if (mbar_try_wait_cluster(a, parity)) return true;
-  const unsigned long long t0 = globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_cluster(a, parity)) return true;
-    if ((i & 63u) == 0) {
-      if (*abort) return false;
-      if (globaltimer_ns() - t0 > limit_ns) {
-        set_status(status, STATUS_WAIT_TIMEOUT);
-        *abort = 1;
-        return false;
-      }
-    }
-  }
-}
+__device__ __forceinline__ void cluster_fence() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 // TMEM of both CTAs of the pair; one whole warp of each CTA takes part.
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {

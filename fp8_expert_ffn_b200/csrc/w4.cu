@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(THREADS, 2)
           for (int c = 0; c < 4; ++c) xr[j][c] = load_x8(xrow[j], kb * KB + c * 32 + t * 8, p.k);
         const uint32_t s = ring.used % STAGES;
         if (ok) {
-          const bool got = mbar_wait(&ring.bar[s], (ring.used / STAGES) & 1u, s_abort, p.status, p.wait_ns);
+          const bool got = mbar_wait_stage(&ring.bar[s], (ring.used / STAGES) & 1u, s_abort, p.status, p.wait_ns);
           ok = __all_sync(0xFFFFFFFFu, got);
         }
         if (ok) {
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   if (lane == 0) {
     int never = 0;
     for (uint32_t j = ring.used; j < ring.issued; ++j)
-      if (j != withheld) mbar_wait(&ring.bar[j % STAGES], (j / STAGES) & 1u, &never, p.status, p.wait_ns);
+      if (j != withheld) mbar_wait_stage(&ring.bar[j % STAGES], (j / STAGES) & 1u, &never, p.status, p.wait_ns);
   }
 }
 
