@@ -32,6 +32,7 @@
 #include "common.cuh"
 #include "groups.cuh"
 #include "internal.h"
+#include "pair.cuh"
 
 namespace moe {
 
@@ -96,10 +97,10 @@ __device__ __forceinline__ uint32_t unpack_pair(uint32_t w, int i, uint32_t bias
   return d;
 }
 
-__device__ __forceinline__ float load_scale(const void* s, int type, size_t i) {
-  if (type == MOE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(s)[i]);
-  if (type == MOE_F16) return __half2float(static_cast<const __half*>(s)[i]);
-  return static_cast<const float*>(s)[i];
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
 }
 
 struct Unit {
@@ -119,9 +120,10 @@ __device__ __forceinline__ Unit decode_unit(int i, const GroupPlan& s, const W4A
   return u;
 }
 
-// 8 values of a row of x from column i on; columns past k are zero.
+// 8 values of a row of x from column i on; columns past k, and rows that are
+// not there, are zero.
 template <typename T>
-__device__ __forceinline__ uint4 load_x8(const T* row, int i, int k) {
+__device__ __forceinline__ uint4 load_x8_edge(const T* row, int i, int k) {
   if (row == nullptr || i >= k) return make_uint4(0u, 0u, 0u, 0u);
   if (i + 8 <= k) return __ldg(reinterpret_cast<const uint4*>(row + i));
   uint32_t v[4] = {0u, 0u, 0u, 0u};
@@ -141,83 +143,117 @@ __device__ __forceinline__ void store_y(const W4Args& p, size_t at, float v) {
     static_cast<__half*>(p.y)[at] = __float2half_rn(v);
 }
 
-// One warp's ring: issues run STAGES blocks ahead of use, across tiles.
-struct Ring {
-  uint8_t* base;        // this warp's stages
-  uint64_t* bar;        // [STAGES]
-  uint32_t used;        // blocks consumed so far
-  uint32_t issued;      // lane 0 only
-  int unit, kb, kb1;    // lane 0 only: next block to issue
-  int g, row;           // lane 0 only: its group and first weight row
+// A lane's part of a block's scales and zero points (rows 16 t + g and
+// 16 t + 8 + g of the warp's 64, t = lane % 4; the lanes of a quad exchange
+// them by shuffles); zero points as nibbles of one word.
+template <int GPB>
+struct Scales {
+  float sc[GPB][2];
+  uint32_t zp;
 };
 
-template <bool BF16, int GS, int NT>
-__device__ __forceinline__ void block_mma(const W4Args& p, const uint8_t* st, float (&acc)[4][NT][4],
-                                          const uint4 (&xr)[NT][4], const size_t (&srow)[4][2], int kb, int lane) {
-  constexpr int GPB = KB / GS;   // scale groups per block
-  constexpr int CPG = GS / 32;   // 32-code chunks per scale group
-  const int g = lane >> 2, t = lane & 3;
-  uint32_t xp[NT][4][4];
+template <bool ZEROS, int GPB>
+__device__ __forceinline__ void load_scales(const W4Args& p, const void* sp, const uint8_t* zp, const int (&srow)[2],
+                                            int kb, Scales<GPB>& o) {
+  const int g0 = kb * GPB;
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+  for (int q = 0; q < GPB; ++q)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      xp[j][c][0] = __byte_perm(xr[j][c].x, xr[j][c].z, 0x5410);
-      xp[j][c][1] = __byte_perm(xr[j][c].x, xr[j][c].z, 0x7632);
-      xp[j][c][2] = __byte_perm(xr[j][c].y, xr[j][c].w, 0x5410);
-      xp[j][c][3] = __byte_perm(xr[j][c].y, xr[j][c].w, 0x7632);
+    for (int h = 0; h < 2; ++h) {
+      // groups past the row's end meet zero x: any finite scale will do
+      const int at = srow[h] + min(g0 + q, p.ng - 1);
+      if (p.scale_type == MOE_F32)
+        o.sc[q][h] = __ldg(static_cast<const float*>(sp) + at);
+      else if (p.scale_type == MOE_BF16)
+        o.sc[q][h] = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(sp) + at)) << 16);
+      else
+        o.sc[q][h] = __half2float(__ldg(static_cast<const __half*>(sp) + at));
     }
-  constexpr uint32_t BASE = BF16 ? 0x43004300u : 0x64006400u;
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    const int which = p.dual ? m >> 1 : 0;
-    float sc[GPB][2];
-    uint32_t bias[GPB][2];
+  if (ZEROS) {
+    o.zp = 0u;
 #pragma unroll
     for (int q = 0; q < GPB; ++q)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int grp = kb * GPB + q;
-        const bool in = grp < p.ng;   // groups past the row's end meet zero x
-        sc[q][h] = in ? load_scale(p.scales[which], p.scale_type, srow[m][h] + grp) : 0.0f;
-        bias[q][h] = BASE + (p.zeros[which] && in ? uint32_t(p.zeros[which][srow[m][h] + grp] & 15) : 8u) * 0x00010001u;
-      }
-    float part[NT][4];
+      for (int h = 0; h < 2; ++h)
+        o.zp |= uint32_t(__ldg(zp + srow[h] + min(g0 + q, p.ng - 1)) & 15) << (4 * (2 * q + h));
+  }
+}
+
+// A lane's 8-column pieces of NT x 8 rows of x in NC 32-column chunks from
+// column `at` on.
+template <typename T, int NT, int NC>
+__device__ __forceinline__ void load_x(const T* const (&xrow)[2], bool edge, int at, int k, uint4 (&x)[NT][NC]) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (c % CPG == 0) {
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      x[j][c] = edge ? load_x8_edge(xrow[j], at + c * 32, k)
+                     : __ldg(reinterpret_cast<const uint4*>(xrow[j] + at + c * 32));
+}
+
+// Chunks [C0, C0 + NC) of 32 codes x 64 weight rows against 8 NT rows of x.
+template <bool BF16, int GS, bool ZEROS, int NT, int C0, int NC>
+__device__ __forceinline__ void chunks_mma(uint32_t st, float (&acc)[4][NT][4], const Scales<KB / GS>& cur,
+                                           const uint4 (&x)[NT][NC], int lane) {
+  constexpr int CPG = GS / 32;   // 32-code chunks per scale group
+  constexpr uint32_t BASE = BF16 ? 0x43004300u : 0x64006400u;
+  const int g = lane >> 2, t = lane & 3;
+  uint32_t xp[NT][NC][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      xp[j][c][0] = __byte_perm(x[j][c].x, x[j][c].z, 0x5410);
+      xp[j][c][1] = __byte_perm(x[j][c].x, x[j][c].z, 0x7632);
+      xp[j][c][2] = __byte_perm(x[j][c].y, x[j][c].w, 0x5410);
+      xp[j][c][3] = __byte_perm(x[j][c].y, x[j][c].w, 0x7632);
+    }
+  // 16-byte chunk c of row r sits at chunk c ^ ((r / 2) % 4)
+  const uint32_t row = st + g * 64 + t * 4;
+  const int sw = (g >> 1) & 3;
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const int src = (lane & ~3) | m;   // the lane that holds this m's scales
+    float part[NT][4];
+    uint32_t zp = 0x88888888u;
+    if (ZEROS) zp = __shfl_sync(0xFFFFFFFFu, cur.zp, src);
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc) {
+      const int c = C0 + cc;
+      const int q = c / CPG;
+      if (cc == 0 || c % CPG == 0) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) part[j][e] = 0.0f;
       }
-      // 16-byte chunk c of row r sits at chunk c ^ ((r / 2) % 4)
-      const int r0 = m * 16 + g;
-      const int o = ((c ^ ((g >> 1) & 3)) << 4) + t * 4;
-      const uint32_t w0 = *reinterpret_cast<const uint32_t*>(st + r0 * 64 + o);
-      const uint32_t w1 = *reinterpret_cast<const uint32_t*>(st + (r0 + 8) * 64 + o);
-      const uint32_t b0 = bias[c / CPG][0], b1 = bias[c / CPG][1];
+      const uint32_t b0 = BASE + ((zp >> (8 * q)) & 15u) * 0x00010001u;
+      const uint32_t b1 = BASE + ((zp >> (8 * q + 4)) & 15u) * 0x00010001u;
+      const int o = (c ^ sw) << 4;
+      const uint32_t w0 = lds32(row + m * 1024 + o), w1 = lds32(row + m * 1024 + 512 + o);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const uint32_t a0 = unpack_pair<BF16>(w0, 2 * s, b0), a1 = unpack_pair<BF16>(w1, 2 * s, b1);
         const uint32_t a2 = unpack_pair<BF16>(w0, 2 * s + 1, b0), a3 = unpack_pair<BF16>(w1, 2 * s + 1, b1);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) mma_16816<BF16>(part[j], a0, a1, a2, a3, xp[j][c][2 * s], xp[j][c][2 * s + 1]);
+        for (int j = 0; j < NT; ++j) mma_16816<BF16>(part[j], a0, a1, a2, a3, xp[j][cc][2 * s], xp[j][cc][2 * s + 1]);
       }
-      if (c % CPG == CPG - 1) {
+      if (cc == NC - 1 || c % CPG == CPG - 1) {
+        const float s0 = __shfl_sync(0xFFFFFFFFu, cur.sc[q][0], src);
+        const float s1 = __shfl_sync(0xFFFFFFFFu, cur.sc[q][1], src);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          acc[m][j][0] = fmaf(part[j][0], sc[c / CPG][0], acc[m][j][0]);
-          acc[m][j][1] = fmaf(part[j][1], sc[c / CPG][0], acc[m][j][1]);
-          acc[m][j][2] = fmaf(part[j][2], sc[c / CPG][1], acc[m][j][2]);
-          acc[m][j][3] = fmaf(part[j][3], sc[c / CPG][1], acc[m][j][3]);
+          acc[m][j][0] = fmaf(part[j][0], s0, acc[m][j][0]);
+          acc[m][j][1] = fmaf(part[j][1], s0, acc[m][j][1]);
+          acc[m][j][2] = fmaf(part[j][2], s1, acc[m][j][2]);
+          acc[m][j][3] = fmaf(part[j][3], s1, acc[m][j][3]);
         }
       }
     }
   }
 }
 
-template <bool BF16, int GS>
+template <bool BF16, int GS, bool ZEROS>
 __global__ void __launch_bounds__(THREADS, 2)
     w4_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1, const W4Args p) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
@@ -228,7 +264,8 @@ __global__ void __launch_bounds__(THREADS, 2)
   volatile int* s_abort = &s_abort_store;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* red = reinterpret_cast<float*>(smem + RING_BYTES);   // [WARPS][64][8]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
   const int wn = WARPS / p.wk;                 // warps along the columns
   const int kw = warp % p.wk, nw = warp / p.wk;
   const int wrows = p.dual ? BOX_ROWS / 2 : BOX_ROWS;   // output columns of a warp
@@ -250,74 +287,71 @@ __global__ void __launch_bounds__(THREADS, 2)
                                         [&](int n_g) -> int { return ((n_g + RMAX - 1) / RMAX) * p.ntn; });
 
   const int kb0 = kw * p.nkb / p.wk, kb1 = (kw + 1) * p.nkb / p.wk;   // this warp's blocks of a tile
-  Ring ring;
-  ring.base = smem + warp * (STAGES * STAGE_BYTES);
-  ring.bar = s_bar[warp];
-  ring.used = 0;
-  ring.issued = 0;
-  ring.unit = int(blockIdx.x);
-  ring.kb = kb0;
-  ring.kb1 = kb1;
+  // The ring runs STAGES blocks ahead of use, across tiles; every lane keeps
+  // its state and one of them issues the copies.
+  const uint32_t ring = smem_u32(smem) + warp * (STAGES * STAGE_BYTES);
+  uint64_t* bar = s_bar[warp];
+  uint32_t used = 0, issued = 0, withheld = 0xFFFFFFFFu;
+  int i_unit = int(blockIdx.x), i_kb = kb0, i_g = 0, i_row = 0;
   bool ok = true;
-  uint32_t withheld = 0xFFFFFFFFu;
-
-  auto place = [&]() {   // lane 0: the group and weight row of ring.unit
-    if (ring.unit < total) {
-      const Unit u = decode_unit(ring.unit, s_plan, p);
-      ring.g = u.g;
-      ring.row = (u.nt * wn + nw) * wrows;
+  auto place = [&]() {   // the group and first weight row of i_unit
+    if (i_unit < total) {
+      const Unit u = decode_unit(i_unit, s_plan, p);
+      i_g = u.g;
+      i_row = (u.nt * wn + nw) * wrows;
     }
   };
-  auto issue = [&]() {   // lane 0: the next block, if there is one
-    if (ring.unit >= total || kb0 == kb1) return;
-    const uint32_t s = ring.issued % STAGES;
-    if (p.withhold && blockIdx.x == 0 && warp == 0 && ring.issued == 0) {
+  auto issue = [&]() {   // the next block, if there is one
+    if (i_unit >= total || kb0 == kb1) return;
+    const uint32_t s = issued % STAGES;
+    if (p.withhold && blockIdx.x == 0 && warp == 0 && issued == 0) {
       withheld = 0;   // test only: this block never arrives
-    } else {
-      uint8_t* dst = ring.base + s * STAGE_BYTES;
-      mbar_arrive_expect_tx(&ring.bar[s], STAGE_BYTES);
-      tma_load_3d(dst, &tm0, &ring.bar[s], ring.kb * (KB / 2), ring.row, ring.g);
-      if (p.dual) tma_load_3d(dst + STAGE_BYTES / 2, &tm1, &ring.bar[s], ring.kb * (KB / 2), ring.row, ring.g);
+    } else if (elect_one()) {
+      uint8_t* dst = smem + (warp * STAGES + s) * STAGE_BYTES;
+      mbar_arrive_expect_tx(&bar[s], STAGE_BYTES);
+      tma_load_3d(dst, &tm0, &bar[s], i_kb * (KB / 2), i_row, i_g);
+      if (p.dual) tma_load_3d(dst + STAGE_BYTES / 2, &tm1, &bar[s], i_kb * (KB / 2), i_row, i_g);
     }
-    ++ring.issued;
-    if (++ring.kb == kb1) {
-      ring.kb = kb0;
-      ring.unit += gridDim.x;
+    ++issued;
+    if (++i_kb == kb1) {
+      i_kb = kb0;
+      i_unit += gridDim.x;
       place();
     }
   };
-  if (lane == 0) {
-    place();
-    for (int s = 0; s < STAGES; ++s) issue();
-  }
+  place();
+  for (int s = 0; s < STAGES; ++s) issue();
   __syncwarp();
 
   for (int i = blockIdx.x; i < total; i += gridDim.x) {
     const Unit u = decode_unit(i, s_plan, p);
-    const int g = lane >> 2, t = lane & 3;
     const int nbase = (u.nt * wn + nw) * wrows;
-    // scale rows of this lane's weight rows (rows past n: the last one's, not stored)
-    size_t srow[4][2];
+    // this lane's scale rows within the group (rows past n: the last one's, not stored)
+    int srow[2];
+    const int which = p.dual ? t >> 1 : 0;
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = nbase + (p.dual ? (m & 1) : m) * 16 + h * 8 + g;
-        srow[m][h] = (size_t(u.g) * p.n + min(r, p.n - 1)) * size_t(p.ng);
-      }
+    for (int h = 0; h < 2; ++h) srow[h] = min(nbase + (p.dual ? (t & 1) : t) * 16 + h * 8 + g, p.n - 1) * p.ng;
+    const size_t gofs = size_t(u.g) * size_t(p.n) * size_t(p.ng);
+    const void* sp = static_cast<const uint8_t*>(p.scales[which]) + gofs * (p.scale_type == MOE_F32 ? 4 : 2);
+    const uint8_t* zp = p.zeros[which] ? p.zeros[which] + gofs : nullptr;
+    // rows of x; those past the chunk feed MMA columns that are not stored
+    // and read the chunk's first row
     const T* xrow[2];
+    bool missing = false;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
+      const int r = u.r0 + (8 * j + g < u.nr ? 8 * j + g : 0);
+      const int tok = p.perm ? __ldg(p.perm + r) : r;
       xrow[j] = nullptr;
-      const int r = 8 * j + g;
-      if (r < u.nr) {
-        const int tok = p.perm ? __ldg(p.perm + u.r0 + r) : u.r0 + r;
-        if (tok >= 0 && tok < p.x_rows)
-          xrow[j] = static_cast<const T*>(p.x) + size_t(tok) * size_t(p.ldx);
-        else
-          set_status(p.status, STATUS_BAD_ROW);
+      if (tok >= 0 && tok < p.x_rows) {
+        xrow[j] = static_cast<const T*>(p.x) + size_t(tok) * size_t(p.ldx);
+      } else {
+        set_status(p.status, STATUS_BAD_ROW);
+        missing = true;
       }
     }
+    missing = __any_sync(0xFFFFFFFFu, missing);
+
     auto tile = [&](auto nt_c) {
       constexpr int NT = decltype(nt_c)::value;
       float acc[4][NT][4];
@@ -327,22 +361,29 @@ __global__ void __launch_bounds__(THREADS, 2)
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.0f;
+      Scales<KB / GS> sc;
       for (int kb = kb0; kb < kb1; ++kb) {
-        uint4 xr[NT][4];   // in flight while the codes arrive
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) xr[j][c] = load_x8(xrow[j], kb * KB + c * 32 + t * 8, p.k);
-        const uint32_t s = ring.used % STAGES;
+        // scales and x are on their way while the codes arrive; 16 rows of x
+        // take as many registers as 8 when the block is done in halves
+        constexpr int NC = 4 / NT;
+        uint4 x[NT][NC];
+        const bool edge = missing || (kb + 1) * KB > p.k;
+        load_x<T, NT, NC>(xrow, edge, kb * KB + t * 8, p.k, x);
+        load_scales<ZEROS>(p, sp, zp, srow, kb, sc);
         if (ok) {
-          const bool got = mbar_wait_stage(&ring.bar[s], (ring.used / STAGES) & 1u, s_abort, p.status, p.wait_ns);
+          const bool got = mbar_wait_stage(&bar[used % STAGES], (used / STAGES) & 1u, s_abort, p.status, p.wait_ns);
           ok = __all_sync(0xFFFFFFFFu, got);
         }
         if (ok) {
-          block_mma<BF16, GS, NT>(p, ring.base + s * STAGE_BYTES, acc, xr, srow, kb, lane);
-          ++ring.used;
+          const uint32_t st = ring + (used % STAGES) * STAGE_BYTES;
+          chunks_mma<BF16, GS, ZEROS, NT, 0, NC>(st, acc, sc, x, lane);
+          if constexpr (NT == 2) {
+            load_x<T, NT, NC>(xrow, edge, kb * KB + 64 + t * 8, p.k, x);
+            chunks_mma<BF16, GS, ZEROS, NT, 2, 2>(st, acc, sc, x, lane);
+          }
+          ++used;
           __syncwarp();   // every lane has read the stage
-          if (lane == 0) issue();
+          issue();
         }
       }
       // partial sums of the warps along the contraction, in warp order
@@ -356,11 +397,12 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         __syncthreads();
         const int cols = wrows * wn;   // output columns of the tile
-        for (int e = threadIdx.x; e < cols * 8; e += THREADS) {
+        const int nr = min(8, u.nr - 8 * j);
+        for (int e = threadIdx.x; e < cols * nr; e += THREADS) {
           const int r = e / cols, c = e - r * cols;
           const int w = c / wrows, cc = c - w * wrows;
           const int col = (u.nt * wn + w) * wrows + cc;
-          if (8 * j + r < u.nr && col < p.n) {
+          if (col < p.n) {
             const float* src = red + size_t(w) * p.wk * (BOX_ROWS * 8) + cc * 8 + r;
             float a = 0.0f, b = 0.0f;
             for (int q = 0; q < p.wk; ++q) a += src[q * (BOX_ROWS * 8)];
@@ -382,17 +424,17 @@ __global__ void __launch_bounds__(THREADS, 2)
   // copies issued but never used (only after an abort) must land first
   if (lane == 0) {
     int never = 0;
-    for (uint32_t j = ring.used; j < ring.issued; ++j)
-      if (j != withheld) mbar_wait_stage(&ring.bar[j % STAGES], (j / STAGES) & 1u, &never, p.status, p.wait_ns);
+    for (uint32_t j = used; j < issued; ++j)
+      if (j != withheld) mbar_wait_stage(&bar[j % STAGES], (j / STAGES) & 1u, &never, p.status, p.wait_ns);
   }
 }
 
-template <bool BF16, int GS>
+template <bool BF16, int GS, bool ZEROS>
 cudaError_t launch(const moe_layer_s* L, const CUtensorMap& tm0, const CUtensorMap& tm1, W4Args a, long long units,
                    cudaStream_t st) {
   static std::atomic<bool> configured[kMaxDevices];   // the attribute is per device
   cudaError_t ce = once_per_device(configured, []() {
-    return cudaFuncSetAttribute(w4_kernel<BF16, GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_DYN);
+    return cudaFuncSetAttribute(w4_kernel<BF16, GS, ZEROS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_DYN);
   });
   if (ce != cudaSuccess) return ce;
   a.wait_ns = kWaitLimitNs;
@@ -403,15 +445,15 @@ cudaError_t launch(const moe_layer_s* L, const CUtensorMap& tm0, const CUtensorM
   }
   const long long cap = 2ll * L->num_sms;
   const dim3 grid(unsigned(units < cap ? units : cap));
-  return launch_pdl(w4_kernel<BF16, GS>, grid, dim3(THREADS), SMEM_DYN, st, tm0, tm1, a);
+  return launch_pdl(w4_kernel<BF16, GS, ZEROS>, grid, dim3(THREADS), SMEM_DYN, st, tm0, tm1, a);
 }
 
-template <bool BF16>
+template <bool BF16, bool ZEROS>
 cudaError_t launch_group(const moe_layer_s* L, int group, const CUtensorMap& tm0, const CUtensorMap& tm1,
                          const W4Args& a, long long units, cudaStream_t st) {
-  if (group == 32) return launch<BF16, 32>(L, tm0, tm1, a, units, st);
-  if (group == 64) return launch<BF16, 64>(L, tm0, tm1, a, units, st);
-  return launch<BF16, 128>(L, tm0, tm1, a, units, st);
+  if (group == 32) return launch<BF16, 32, ZEROS>(L, tm0, tm1, a, units, st);
+  if (group == 64) return launch<BF16, 64, ZEROS>(L, tm0, tm1, a, units, st);
+  return launch<BF16, 128, ZEROS>(L, tm0, tm1, a, units, st);
 }
 
 }  // namespace
@@ -458,8 +500,11 @@ cudaError_t launch_w4(const moe_layer_s* L, moe_dtype t, const void* x, int x_ro
   tm1 = tm0;
   if (up && !encode_tmap_codes(&tm1, up->codes, (k + 1) / 2, n, G, up->ld, box)) return cudaErrorInvalidValue;
   const long long units = (static_cast<long long>(rows) / RMAX + (rows < G ? rows : G)) * p.ntn;
-  return t == MOE_BF16 ? launch_group<true>(L, w->group, tm0, tm1, p, units, st)
-                       : launch_group<false>(L, w->group, tm0, tm1, p, units, st);
+  if (t == MOE_BF16)
+    return w->zeros ? launch_group<true, true>(L, w->group, tm0, tm1, p, units, st)
+                    : launch_group<true, false>(L, w->group, tm0, tm1, p, units, st);
+  return w->zeros ? launch_group<false, true>(L, w->group, tm0, tm1, p, units, st)
+                  : launch_group<false, false>(L, w->group, tm0, tm1, p, units, st);
 }
 
 }  // namespace moe
