@@ -22,8 +22,8 @@
 // boxes (64 rows x 64 bytes = 128 codes, 64-byte swizzle: lane (g, t) reads
 // word t of row g without bank conflicts), so no warp waits for another until
 // a tile's partial sums meet in shared memory, added in warp order. The warps
-// of a CTA split the contraction 8, 4, 2 or 1 ways (and the columns by the
-// rest), whichever leaves the fewest idle.
+// of a CTA split the contraction 8, 4, 2 or 1 ways and the columns by the
+// rest (see launch_w4).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -113,7 +113,7 @@ __device__ __forceinline__ Unit decode_unit(int i, const GroupPlan& s, const W4A
   const int local = i - s.prefix[u.g];
   const int n_g = s.off[u.g + 1] - s.off[u.g];
   const int chunks = (n_g + RMAX - 1) / RMAX;
-  u.nt = local / chunks;   // the chunks that share codes run side by side
+  u.nt = chunks == 1 ? local : local / chunks;   // the chunks that share codes run side by side
   const int c = local - u.nt * chunks;
   u.r0 = s.off[u.g] + c * RMAX;
   u.nr = min(RMAX, n_g - c * RMAX);
@@ -155,27 +155,32 @@ struct Scales {
 template <bool ZEROS, int GPB>
 __device__ __forceinline__ void load_scales(const W4Args& p, const void* sp, const uint8_t* zp, const int (&srow)[2],
                                             int kb, Scales<GPB>& o) {
-  const int g0 = kb * GPB;
+  int at[GPB];   // groups past the row's end meet zero x: any finite scale will do
 #pragma unroll
-  for (int q = 0; q < GPB; ++q)
+  for (int q = 0; q < GPB; ++q) at[q] = min(kb * GPB + q, p.ng - 1);
+  if (p.scale_type == MOE_BF16) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      // groups past the row's end meet zero x: any finite scale will do
-      const int at = srow[h] + min(g0 + q, p.ng - 1);
-      if (p.scale_type == MOE_F32)
-        o.sc[q][h] = __ldg(static_cast<const float*>(sp) + at);
-      else if (p.scale_type == MOE_BF16)
-        o.sc[q][h] = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(sp) + at)) << 16);
-      else
-        o.sc[q][h] = __half2float(__ldg(static_cast<const __half*>(sp) + at));
-    }
+    for (int q = 0; q < GPB; ++q)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        o.sc[q][h] = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(sp) + (srow[h] + at[q]))) << 16);
+  } else if (p.scale_type == MOE_F16) {
+#pragma unroll
+    for (int q = 0; q < GPB; ++q)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) o.sc[q][h] = __half2float(__ldg(static_cast<const __half*>(sp) + (srow[h] + at[q])));
+  } else {
+#pragma unroll
+    for (int q = 0; q < GPB; ++q)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) o.sc[q][h] = __ldg(static_cast<const float*>(sp) + (srow[h] + at[q]));
+  }
   if (ZEROS) {
     o.zp = 0u;
 #pragma unroll
     for (int q = 0; q < GPB; ++q)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        o.zp |= uint32_t(__ldg(zp + srow[h] + min(g0 + q, p.ng - 1)) & 15) << (4 * (2 * q + h));
+      for (int h = 0; h < 2; ++h) o.zp |= uint32_t(__ldg(zp + (srow[h] + at[q])) & 15) << (4 * (2 * q + h));
   }
 }
 
@@ -183,12 +188,17 @@ __device__ __forceinline__ void load_scales(const W4Args& p, const void* sp, con
 // column `at` on.
 template <typename T, int NT, int NC>
 __device__ __forceinline__ void load_x(const T* const (&xrow)[2], bool edge, int at, int k, uint4 (&x)[NT][NC]) {
+  if (!edge) {
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-      x[j][c] = edge ? load_x8_edge(xrow[j], at + c * 32, k)
-                     : __ldg(reinterpret_cast<const uint4*>(xrow[j] + at + c * 32));
+      for (int c = 0; c < NC; ++c) x[j][c] = __ldg(reinterpret_cast<const uint4*>(xrow[j] + at + c * 32));
+  } else {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) x[j][c] = load_x8_edge(xrow[j], at + c * 32, k);
+  }
 }
 
 // Chunks [C0, C0 + NC) of 32 codes x 64 weight rows against 8 NT rows of x.
@@ -253,6 +263,14 @@ __device__ __forceinline__ void chunks_mma(uint32_t st, float (&acc)[4][NT][4], 
   }
 }
 
+// Barrier of the wk warps that share columns (number nw of the block).
+__device__ __forceinline__ void column_sync(int nw, int wk) {
+  if (wk == 1)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(nw + 1), "r"(wk * 32) : "memory");
+}
+
 template <bool BF16, int GS, bool ZEROS>
 __global__ void __launch_bounds__(THREADS, 2)
     w4_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1, const W4Args p) {
@@ -291,7 +309,8 @@ __global__ void __launch_bounds__(THREADS, 2)
   // its state and one of them issues the copies.
   const uint32_t ring = smem_u32(smem) + warp * (STAGES * STAGE_BYTES);
   uint64_t* bar = s_bar[warp];
-  uint32_t used = 0, issued = 0, withheld = 0xFFFFFFFFu;
+  uint32_t used = 0, issued = 0;
+  const uint32_t withheld = p.withhold && blockIdx.x == 0 ? 0u : 0xFFFFFFFFu;
   int i_unit = int(blockIdx.x), i_kb = kb0, i_g = 0, i_row = 0;
   bool ok = true;
   auto place = [&]() {   // the group and first weight row of i_unit
@@ -304,8 +323,8 @@ __global__ void __launch_bounds__(THREADS, 2)
   auto issue = [&]() {   // the next block, if there is one
     if (i_unit >= total || kb0 == kb1) return;
     const uint32_t s = issued % STAGES;
-    if (p.withhold && blockIdx.x == 0 && warp == 0 && issued == 0) {
-      withheld = 0;   // test only: this block never arrives
+    if (issued == withheld) {
+      // test only: this block never arrives
     } else if (elect_one()) {
       uint8_t* dst = smem + (warp * STAGES + s) * STAGE_BYTES;
       mbar_arrive_expect_tx(&bar[s], STAGE_BYTES);
@@ -395,25 +414,22 @@ __global__ void __launch_bounds__(THREADS, 2)
           *reinterpret_cast<float2*>(mine + (m * 16 + g) * 8 + 2 * t) = make_float2(acc[m][j][0], acc[m][j][1]);
           *reinterpret_cast<float2*>(mine + (m * 16 + g + 8) * 8 + 2 * t) = make_float2(acc[m][j][2], acc[m][j][3]);
         }
-        __syncthreads();
-        const int cols = wrows * wn;   // output columns of the tile
+        column_sync(nw, p.wk);
         const int nr = min(8, u.nr - 8 * j);
-        for (int e = threadIdx.x; e < cols * nr; e += THREADS) {
-          const int r = e / cols, c = e - r * cols;
-          const int w = c / wrows, cc = c - w * wrows;
-          const int col = (u.nt * wn + w) * wrows + cc;
-          if (col < p.n) {
-            const float* src = red + size_t(w) * p.wk * (BOX_ROWS * 8) + cc * 8 + r;
+        for (int e = kw * 32 + lane; e < wrows * nr; e += p.wk * 32) {
+          const int r = p.dual ? e >> 5 : e >> 6, cc = e & (wrows - 1);
+          if (nbase + cc < p.n) {
+            const float* src = red + nw * p.wk * (BOX_ROWS * 8) + cc * 8 + r;
             float a = 0.0f, b = 0.0f;
             for (int q = 0; q < p.wk; ++q) a += src[q * (BOX_ROWS * 8)];
             if (p.dual) {
               for (int q = 0; q < p.wk; ++q) b += src[q * (BOX_ROWS * 8) + wrows * 8];
               a = a / (1.0f + expf(-a)) * b;
             }
-            store_y(p, size_t(u.r0 + 8 * j + r) * size_t(p.ldy) + col, a);
+            store_y(p, size_t(u.r0 + 8 * j + r) * size_t(p.ldy) + size_t(nbase + cc), a);
           }
         }
-        __syncthreads();   // the partial sums are rewritten
+        column_sync(nw, p.wk);   // the partial sums are rewritten
       }
     };
     if (u.nr > 8)
@@ -481,12 +497,21 @@ cudaError_t launch_w4(const moe_layer_s* L, moe_dtype t, const void* x, int x_ro
   p.ng = (k + w->group - 1) / w->group;
   p.dual = up != nullptr;
   p.nkb = (k + KB - 1) / KB;
-  // warps along the contraction: the split that leaves the fewest of their
-  // block slots idle (the widest of equals)
-  p.wk = WARPS;
-  for (int wk = WARPS / 2; wk >= 1; wk /= 2) {
-    const int idle = (p.nkb + wk - 1) / wk * wk - p.nkb, best = (p.nkb + p.wk - 1) / p.wk * p.wk - p.nkb;
-    if (idle < best) p.wk = wk;
+  // Warps along the contraction. More of them give more, smaller units (the
+  // only way to fill the machine with few experts), fewer leave more blocks
+  // per unit to pay for its fixed cost (finding it, joining the partial sums:
+  // about one block's time). The split with the shortest longest CTA:
+  const long long groups = rows / RMAX + (rows < G ? rows : G);   // units per column tile, at most
+  long long best = 0;
+  for (int wk = WARPS; wk >= 1; wk /= 2) {
+    const int cols = (WARPS / wk) * (p.dual ? BOX_ROWS / 2 : BOX_ROWS);
+    const long long units = groups * ((n + cols - 1) / cols);
+    const long long rounds = (units + 2 * L->num_sms - 1) / (2 * L->num_sms);
+    const long long cost = rounds * ((p.nkb + wk - 1) / wk + 1);
+    if (best == 0 || cost < best) {
+      best = cost;
+      p.wk = wk;
+    }
   }
   const int cols = (WARPS / p.wk) * (p.dual ? BOX_ROWS / 2 : BOX_ROWS);
   p.ntn = (n + cols - 1) / cols;
@@ -499,7 +524,7 @@ cudaError_t launch_w4(const moe_layer_s* L, moe_dtype t, const void* x, int x_ro
   if (!encode_tmap_codes(&tm0, w->codes, (k + 1) / 2, n, G, w->ld, box)) return cudaErrorInvalidValue;
   tm1 = tm0;
   if (up && !encode_tmap_codes(&tm1, up->codes, (k + 1) / 2, n, G, up->ld, box)) return cudaErrorInvalidValue;
-  const long long units = (static_cast<long long>(rows) / RMAX + (rows < G ? rows : G)) * p.ntn;
+  const long long units = groups * p.ntn;
   if (t == MOE_BF16)
     return w->zeros ? launch_group<true, true>(L, w->group, tm0, tm1, p, units, st)
                     : launch_group<true, false>(L, w->group, tm0, tm1, p, units, st);
