@@ -69,6 +69,7 @@ struct W4Args {
   uint32_t* status;
   unsigned long long wait_ns;
   int withhold;
+  uint32_t mask;              // 0x000F000F (see unpack_pair)
 };
 
 template <bool BF16>
@@ -85,11 +86,13 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 }
 
 // Nibbles i and i + 4 of w, less the zero point, as a 16-bit pair;
-// bias = (128 + z, twice) in bf16 or (1024 + z, twice) in fp16.
+// bias = (128 + z, twice) in bf16 or (1024 + z, twice) in fp16. mask is
+// 0x000F000F in a register: lop3 takes one immediate, and as a second one the
+// mask costs an instruction of its own in every pair.
 template <bool BF16>
-__device__ __forceinline__ uint32_t unpack_pair(uint32_t w, int i, uint32_t bias) {
-  uint32_t v = ((w >> (4 * i)) & 0x000F000Fu) | (BF16 ? 0x43004300u : 0x64006400u);
-  uint32_t d;
+__device__ __forceinline__ uint32_t unpack_pair(uint32_t w, int i, uint32_t bias, uint32_t mask) {
+  uint32_t v, d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w >> (4 * i)), "r"(mask), "n"(BF16 ? 0x43004300 : 0x64006400));
   if (BF16)
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(bias));
   else
@@ -204,7 +207,7 @@ __device__ __forceinline__ void load_x(const T* const (&xrow)[2], bool edge, int
 // Chunks [C0, C0 + NC) of 32 codes x 64 weight rows against 8 NT rows of x.
 template <bool BF16, int GS, bool ZEROS, int NT, int C0, int NC>
 __device__ __forceinline__ void chunks_mma(uint32_t st, float (&acc)[4][NT][4], const Scales<KB / GS>& cur,
-                                           const uint4 (&x)[NT][NC], int lane) {
+                                           const uint4 (&x)[NT][NC], int lane, uint32_t mask) {
   constexpr int CPG = GS / 32;   // 32-code chunks per scale group
   constexpr uint32_t BASE = BF16 ? 0x43004300u : 0x64006400u;
   const int g = lane >> 2, t = lane & 3;
@@ -243,8 +246,8 @@ __device__ __forceinline__ void chunks_mma(uint32_t st, float (&acc)[4][NT][4], 
       const uint32_t w0 = lds32(row + m * 1024 + o), w1 = lds32(row + m * 1024 + 512 + o);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const uint32_t a0 = unpack_pair<BF16>(w0, 2 * s, b0), a1 = unpack_pair<BF16>(w1, 2 * s, b1);
-        const uint32_t a2 = unpack_pair<BF16>(w0, 2 * s + 1, b0), a3 = unpack_pair<BF16>(w1, 2 * s + 1, b1);
+        const uint32_t a0 = unpack_pair<BF16>(w0, 2 * s, b0, mask), a1 = unpack_pair<BF16>(w1, 2 * s, b1, mask);
+        const uint32_t a2 = unpack_pair<BF16>(w0, 2 * s + 1, b0, mask), a3 = unpack_pair<BF16>(w1, 2 * s + 1, b1, mask);
 #pragma unroll
         for (int j = 0; j < NT; ++j) mma_16816<BF16>(part[j], a0, a1, a2, a3, xp[j][cc][2 * s], xp[j][cc][2 * s + 1]);
       }
@@ -395,10 +398,10 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         if (ok) {
           const uint32_t st = ring + (used % STAGES) * STAGE_BYTES;
-          chunks_mma<BF16, GS, ZEROS, NT, 0, NC>(st, acc, sc, x, lane);
+          chunks_mma<BF16, GS, ZEROS, NT, 0, NC>(st, acc, sc, x, lane, p.mask);
           if constexpr (NT == 2) {
             load_x<T, NT, NC>(xrow, edge, kb * KB + 64 + t * 8, p.k, x);
-            chunks_mma<BF16, GS, ZEROS, NT, 2, 2>(st, acc, sc, x, lane);
+            chunks_mma<BF16, GS, ZEROS, NT, 2, 2>(st, acc, sc, x, lane, p.mask);
           }
           ++used;
           __syncwarp();   // every lane has read the stage
@@ -519,6 +522,7 @@ cudaError_t launch_w4(const moe_layer_s* L, moe_dtype t, const void* x, int x_ro
   p.ldy = ldy;
   p.y_type = out_t;
   p.status = L->status;
+  p.mask = 0x000F000Fu;
   CUtensorMap tm0, tm1;
   const uint32_t box = p.dual ? BOX_ROWS / 2 : BOX_ROWS;
   if (!encode_tmap_codes(&tm0, w->codes, (k + 1) / 2, n, G, w->ld, box)) return cudaErrorInvalidValue;
