@@ -189,7 +189,7 @@ bool encode_tmap(CUtensorMap* tm, bool bf16, const void* base, uint64_t inner, u
 bool encode_tmap_16(CUtensorMap* tm, moe_dtype t, const void* base, uint64_t inner, uint64_t rows, uint64_t depth,
                     uint64_t ld, uint32_t box_inner, uint32_t box_rows);
 // Map of 4-bit codes [depth][rows][inner bytes], row stride `ld` bytes, boxes
-// of box_rows x 64 bytes with 64-byte swizzle.
+// of box_rows x 128 bytes with 128-byte swizzle.
 bool encode_tmap_codes(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t rows, uint64_t depth, uint64_t ld,
                        uint32_t box_rows);
 // Products grouped by expert in 16-bit types (gmm.cu). forward and dgrad:

@@ -38,15 +38,17 @@ namespace moe {
 
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 constexpr int WARPS = THREADS / 32;
-constexpr int KB = 128;                    // codes per row of a block
+constexpr int CTAS_PER_SM = 3;
+constexpr int KB = 256;                    // codes per row of a stage
+constexpr int KH = KB / 2;                 // and of the half that is worked on at a time
 constexpr int STAGES = 2;
 constexpr int BOX_ROWS = 64;
-constexpr int STAGE_BYTES = BOX_ROWS * KB / 2;   // 4 KB
-constexpr int RMAX = 16;                   // rows of a chunk
+constexpr int STAGE_BYTES = BOX_ROWS * KB / 2;   // 8 KB
 constexpr int RING_BYTES = WARPS * STAGES * STAGE_BYTES;
-constexpr int RED_BYTES = WARPS * BOX_ROWS * 8 * 4;   // partial sums of 8 rows
+constexpr int RED_ROWS = BOX_ROWS / 2;                // weight rows joined at a time
+constexpr int RED_BYTES = WARPS * RED_ROWS * 8 * 4;   // their partial sums for 8 rows of x
 constexpr int SMEM_DYN = RING_BYTES + RED_BYTES + 1024;
 
 struct W4Args {
@@ -59,6 +61,7 @@ struct W4Args {
   const void* scales[2];      // gate (or the only weight), up
   const uint8_t* zeros[2];
   int scale_type;
+  int vec;                    // a row's scales of a stage are one aligned vector of 16-bit values
   int n, k, ng;               // ng: scale groups of a weight row
   int dual;                   // gate/up form
   int wk;                     // warps along the contraction
@@ -106,10 +109,49 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   return v;
 }
 
+// Read-only loads that stay where they are written (ahead of the wait that
+// their latency hides under), which the compiler would not leave __ldg to do.
+__device__ __forceinline__ uint4 ldg128(const void* a) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 ldg128_or_zero(const void* a, bool there) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "@p ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+      : "l"(a), "r"(int(there)));
+  return v;
+}
+__device__ __forceinline__ uint2 ldg64(const void* a) {
+  uint2 v;
+  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t ldg32(const void* a) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t ldg16(const void* a) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .u16 h;\n\tld.global.nc.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "l"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t ldg8(const void* a) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(a));
+  return v;
+}
+
 struct Unit {
-  int g, nt, r0, nr;   // group, column tile, first row, rows (at most RMAX)
+  int g, nt, r0, nr;   // group, column tile, first row, rows (at most 8 NT)
 };
 
+template <int RMAX>
 __device__ __forceinline__ Unit decode_unit(int i, const GroupPlan& s, const W4Args& p) {
   Unit u;
   u.g = find_group(s.prefix, p.ngroups, i);
@@ -146,56 +188,103 @@ __device__ __forceinline__ void store_y(const W4Args& p, size_t at, float v) {
     static_cast<__half*>(p.y)[at] = __float2half_rn(v);
 }
 
-// A lane's part of a block's scales and zero points (rows 16 t + g and
+// A lane's part of a stage's scales and zero points (rows 16 t + g and
 // 16 t + 8 + g of the warp's 64, t = lane % 4; the lanes of a quad exchange
-// them by shuffles); zero points as nibbles of one word.
-template <int GPB>
+// them by shuffles). They are kept as loaded until their use: converting them
+// at the load would wait for it. 16-bit scales are packed in pairs.
+template <int GPS>
 struct Scales {
-  float sc[GPB][2];
-  uint32_t zp;
+  uint32_t raw[2][GPS];
+  uint32_t zero[2][GPS / 2 < 1 ? 1 : GPS / 2];   // byte pairs
 };
 
-template <bool ZEROS, int GPB>
+// Where every row's scales of a stage are one aligned vector (p.vec), they
+// come in one load: 64 rows are as many cache lines, and a load per scale
+// spends its time there (T = 64 gate/up: 39 of 455 us).
+template <bool ZEROS, int GPS>
 __device__ __forceinline__ void load_scales(const W4Args& p, const void* sp, const uint8_t* zp, const int (&srow)[2],
-                                            int kb, Scales<GPB>& o) {
-  int at[GPB];   // groups past the row's end meet zero x: any finite scale will do
+                                            int kb, Scales<GPS>& o) {
+  const int g0 = kb * GPS;
 #pragma unroll
-  for (int q = 0; q < GPB; ++q) at[q] = min(kb * GPB + q, p.ng - 1);
-  if (p.scale_type == MOE_BF16) {
+  for (int h = 0; h < 2; ++h) {
+    if (p.vec) {
+      const uint16_t* a = static_cast<const uint16_t*>(sp) + (srow[h] + g0);
+      if (GPS == 2) {
+        o.raw[h][0] = ldg32(a);
+      } else if (GPS == 4) {
+        const uint2 v = ldg64(a);
+        o.raw[h][0] = v.x;
+        o.raw[h][1] = v.y;
+      } else {
+        const uint4 v = ldg128(a);
+        o.raw[h][0] = v.x;
+        o.raw[h][1] = v.y;
+        o.raw[h][2] = v.z;
+        o.raw[h][3] = v.w;
+      }
+      if (ZEROS) {
+        const uint8_t* z = zp + (srow[h] + g0);
+        if (GPS == 2) {
+          o.zero[h][0] = ldg16(z);
+        } else if (GPS == 4) {
+          o.zero[h][0] = ldg32(z);
+        } else {
+          const uint2 v = ldg64(z);
+          o.zero[h][0] = v.x;
+          o.zero[h][1] = v.y;
+        }
+      }
+    } else {
 #pragma unroll
-    for (int q = 0; q < GPB; ++q)
+      for (int q = 0; q < GPS; ++q) {
+        const int at = srow[h] + min(g0 + q, p.ng - 1);   // groups past the row's end meet zero x
+        o.raw[h][q] = p.scale_type == MOE_F32 ? ldg32(static_cast<const uint32_t*>(sp) + at)
+                                              : ldg16(static_cast<const uint16_t*>(sp) + at);
+      }
+      if (ZEROS) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        o.sc[q][h] = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(sp) + (srow[h] + at[q]))) << 16);
-  } else if (p.scale_type == MOE_F16) {
-#pragma unroll
-    for (int q = 0; q < GPB; ++q)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) o.sc[q][h] = __half2float(__ldg(static_cast<const __half*>(sp) + (srow[h] + at[q])));
-  } else {
-#pragma unroll
-    for (int q = 0; q < GPB; ++q)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) o.sc[q][h] = __ldg(static_cast<const float*>(sp) + (srow[h] + at[q]));
+        for (int q = 0; q < GPS; q += 2)
+          o.zero[h][q / 2] = ldg8(zp + srow[h] + min(g0 + q, p.ng - 1)) |
+                             (ldg8(zp + srow[h] + min(g0 + q + 1, p.ng - 1)) << 8);
+      }
+    }
   }
-  if (ZEROS) {
-    o.zp = 0u;
+}
+
+// Half H of a stage's scales as floats and zero points as nibbles of a word.
+template <bool ZEROS, int GPS, int H>
+__device__ __forceinline__ void unpack_scales(const W4Args& p, const Scales<GPS>& s, float (&f)[GPS / 2][2],
+                                              uint32_t& zp) {
+  constexpr int GPB = GPS / 2;
+  zp = 0u;
 #pragma unroll
-    for (int q = 0; q < GPB; ++q)
+  for (int q = 0; q < GPB; ++q)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) o.zp |= uint32_t(__ldg(zp + (srow[h] + at[q])) & 15) << (4 * (2 * q + h));
-  }
+    for (int h = 0; h < 2; ++h) {
+      const int i = H * GPB + q;
+      uint32_t v = p.vec ? s.raw[h][i / 2] >> (16 * (i & 1)) : s.raw[h][i];
+      if (p.scale_type == MOE_BF16)
+        v <<= 16;
+      else if (p.scale_type == MOE_F16)
+        v = __float_as_uint(__half2float(__ushort_as_half(uint16_t(v))));
+      f[q][h] = __uint_as_float(v);
+      if (ZEROS) {
+        // vec: four bytes a word; else a byte pair a word
+        const uint32_t z = p.vec ? s.zero[h][i / 4] >> (8 * (i & 3)) : s.zero[h][i / 2] >> (8 * (i & 1));
+        zp |= (z & 15u) << (4 * (2 * q + h));
+      }
+    }
 }
 
 // A lane's 8-column pieces of NT x 8 rows of x in NC 32-column chunks from
 // column `at` on.
 template <typename T, int NT, int NC>
-__device__ __forceinline__ void load_x(const T* const (&xrow)[2], bool edge, int at, int k, uint4 (&x)[NT][NC]) {
+__device__ __forceinline__ void load_x(const T* const (&xrow)[NT], bool edge, int at, int k, uint4 (&x)[NT][NC]) {
   if (!edge) {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int c = 0; c < NC; ++c) x[j][c] = __ldg(reinterpret_cast<const uint4*>(xrow[j] + at + c * 32));
+      for (int c = 0; c < NC; ++c) x[j][c] = ldg128_or_zero(xrow[j] + at + c * 32, xrow[j] != nullptr);
   } else {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -204,56 +293,61 @@ __device__ __forceinline__ void load_x(const T* const (&xrow)[2], bool edge, int
   }
 }
 
-// Chunks [C0, C0 + NC) of 32 codes x 64 weight rows against 8 NT rows of x.
-template <bool BF16, int GS, bool ZEROS, int NT, int C0, int NC>
-__device__ __forceinline__ void chunks_mma(uint32_t st, float (&acc)[4][NT][4], const Scales<KB / GS>& cur,
-                                           const uint4 (&x)[NT][NC], int lane, uint32_t mask) {
+// Half H of a stage, four chunks of 32 codes x 64 weight rows, against 8 NT
+// rows of x.
+template <bool BF16, int GS, bool ZEROS, int NT, int H>
+__device__ __forceinline__ void half_mma(const W4Args& p, uint32_t st, float (&acc)[4][NT][4],
+                                         const Scales<KB / GS>& cur, const uint4 (&x)[NT][4], int lane) {
+  constexpr int GPB = KH / GS;   // scale groups of a half
   constexpr int CPG = GS / 32;   // 32-code chunks per scale group
   constexpr uint32_t BASE = BF16 ? 0x43004300u : 0x64006400u;
   const int g = lane >> 2, t = lane & 3;
-  uint32_t xp[NT][NC][4];
+  const uint32_t mask = p.mask;
+  float sc[GPB][2];
+  uint32_t zp;
+  unpack_scales<ZEROS, KB / GS, H>(p, cur, sc, zp);
+  uint32_t xp[NT][4][4];
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
+    for (int c = 0; c < 4; ++c) {
       xp[j][c][0] = __byte_perm(x[j][c].x, x[j][c].z, 0x5410);
       xp[j][c][1] = __byte_perm(x[j][c].x, x[j][c].z, 0x7632);
       xp[j][c][2] = __byte_perm(x[j][c].y, x[j][c].w, 0x5410);
       xp[j][c][3] = __byte_perm(x[j][c].y, x[j][c].w, 0x7632);
     }
-  // 16-byte chunk c of row r sits at chunk c ^ ((r / 2) % 4)
-  const uint32_t row = st + g * 64 + t * 4;
-  const int sw = (g >> 1) & 3;
+  // 16-byte chunk c of row r sits at chunk c ^ (r % 8)
+  const uint32_t row = st + g * 128 + t * 4;
 #pragma unroll
   for (int m = 0; m < 4; ++m) {
     const int src = (lane & ~3) | m;   // the lane that holds this m's scales
     float part[NT][4];
-    uint32_t zp = 0x88888888u;
-    if (ZEROS) zp = __shfl_sync(0xFFFFFFFFu, cur.zp, src);
+    uint32_t zm = 0x88888888u;
+    if (ZEROS) zm = __shfl_sync(0xFFFFFFFFu, zp, src);
 #pragma unroll
-    for (int cc = 0; cc < NC; ++cc) {
-      const int c = C0 + cc;
+    for (int c = 0; c < 4; ++c) {
       const int q = c / CPG;
-      if (cc == 0 || c % CPG == 0) {
+      if (c % CPG == 0) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) part[j][e] = 0.0f;
       }
-      const uint32_t b0 = BASE + ((zp >> (8 * q)) & 15u) * 0x00010001u;
-      const uint32_t b1 = BASE + ((zp >> (8 * q + 4)) & 15u) * 0x00010001u;
-      const int o = (c ^ sw) << 4;
-      const uint32_t w0 = lds32(row + m * 1024 + o), w1 = lds32(row + m * 1024 + 512 + o);
+      const uint32_t b0 = BASE + ((zm >> (8 * q)) & 15u) * 0x00010001u;
+      const uint32_t b1 = BASE + ((zm >> (8 * q + 4)) & 15u) * 0x00010001u;
+      const uint32_t at = row + m * 2048 + (((4 * H + c) ^ g) << 4);
+      const uint32_t w0 = lds32(at), w1 = lds32(at + 1024);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const uint32_t a0 = unpack_pair<BF16>(w0, 2 * s, b0, mask), a1 = unpack_pair<BF16>(w1, 2 * s, b1, mask);
-        const uint32_t a2 = unpack_pair<BF16>(w0, 2 * s + 1, b0, mask), a3 = unpack_pair<BF16>(w1, 2 * s + 1, b1, mask);
+        const uint32_t a2 = unpack_pair<BF16>(w0, 2 * s + 1, b0, mask);
+        const uint32_t a3 = unpack_pair<BF16>(w1, 2 * s + 1, b1, mask);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) mma_16816<BF16>(part[j], a0, a1, a2, a3, xp[j][cc][2 * s], xp[j][cc][2 * s + 1]);
+        for (int j = 0; j < NT; ++j) mma_16816<BF16>(part[j], a0, a1, a2, a3, xp[j][c][2 * s], xp[j][c][2 * s + 1]);
       }
-      if (cc == NC - 1 || c % CPG == CPG - 1) {
-        const float s0 = __shfl_sync(0xFFFFFFFFu, cur.sc[q][0], src);
-        const float s1 = __shfl_sync(0xFFFFFFFFu, cur.sc[q][1], src);
+      if (c % CPG == CPG - 1) {
+        const float s0 = __shfl_sync(0xFFFFFFFFu, sc[q][0], src);
+        const float s1 = __shfl_sync(0xFFFFFFFFu, sc[q][1], src);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           acc[m][j][0] = fmaf(part[j][0], s0, acc[m][j][0]);
@@ -274,17 +368,18 @@ __device__ __forceinline__ void column_sync(int nw, int wk) {
     asm volatile("bar.sync %0, %1;" ::"r"(nw + 1), "r"(wk * 32) : "memory");
 }
 
-template <bool BF16, int GS, bool ZEROS>
-__global__ void __launch_bounds__(THREADS, 2)
+template <bool BF16, int GS, bool ZEROS, int NT>
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     w4_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1, const W4Args p) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  constexpr int RMAX = 8 * NT;   // rows of a unit
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_bar[WARPS][STAGES];
   __shared__ GroupPlan s_plan;
   __shared__ int s_abort_store;
   volatile int* s_abort = &s_abort_store;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* red = reinterpret_cast<float*>(smem + RING_BYTES);   // [WARPS][64][8]
+  float* red = reinterpret_cast<float*>(smem + RING_BYTES);   // [WARPS][RED_ROWS][8]
   const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int wn = WARPS / p.wk;                 // warps along the columns
@@ -318,7 +413,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   bool ok = true;
   auto place = [&]() {   // the group and first weight row of i_unit
     if (i_unit < total) {
-      const Unit u = decode_unit(i_unit, s_plan, p);
+      const Unit u = decode_unit<RMAX>(i_unit, s_plan, p);
       i_g = u.g;
       i_row = (u.nt * wn + nw) * wrows;
     }
@@ -346,7 +441,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   __syncwarp();
 
   for (int i = blockIdx.x; i < total; i += gridDim.x) {
-    const Unit u = decode_unit(i, s_plan, p);
+    const Unit u = decode_unit<RMAX>(i, s_plan, p);
     const int nbase = (u.nt * wn + nw) * wrows;
     // this lane's scale rows within the group (rows past n: the last one's, not stored)
     int srow[2];
@@ -356,89 +451,92 @@ __global__ void __launch_bounds__(THREADS, 2)
     const size_t gofs = size_t(u.g) * size_t(p.n) * size_t(p.ng);
     const void* sp = static_cast<const uint8_t*>(p.scales[which]) + gofs * (p.scale_type == MOE_F32 ? 4 : 2);
     const uint8_t* zp = p.zeros[which] ? p.zeros[which] + gofs : nullptr;
-    // rows of x; those past the chunk feed MMA columns that are not stored
-    // and read the chunk's first row
-    const T* xrow[2];
-    bool missing = false;
+    // rows of x; rows that are not there (past the unit's, or a perm outside
+    // x) read as zero
+    const T* xrow[NT];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int r = u.r0 + (8 * j + g < u.nr ? 8 * j + g : 0);
-      const int tok = p.perm ? __ldg(p.perm + r) : r;
+    for (int j = 0; j < NT; ++j) {
       xrow[j] = nullptr;
-      if (tok >= 0 && tok < p.x_rows) {
-        xrow[j] = static_cast<const T*>(p.x) + size_t(tok) * size_t(p.ldx);
-      } else {
-        set_status(p.status, STATUS_BAD_ROW);
-        missing = true;
+      if (8 * j + g < u.nr) {
+        const int r = u.r0 + 8 * j + g;
+        const int tok = p.perm ? __ldg(p.perm + r) : r;
+        if (tok >= 0 && tok < p.x_rows)
+          xrow[j] = static_cast<const T*>(p.x) + size_t(tok) * size_t(p.ldx);
+        else
+          set_status(p.status, STATUS_BAD_ROW);
       }
     }
-    missing = __any_sync(0xFFFFFFFFu, missing);
-
-    auto tile = [&](auto nt_c) {
-      constexpr int NT = decltype(nt_c)::value;
-      float acc[4][NT][4];
+    float acc[4][NT][4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m)
+    for (int m = 0; m < 4; ++m)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.0f;
-      Scales<KB / GS> sc;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        // scales and x are on their way while the codes arrive; 16 rows of x
-        // take as many registers as 8 when the block is done in halves
-        constexpr int NC = 4 / NT;
-        uint4 x[NT][NC];
-        const bool edge = missing || (kb + 1) * KB > p.k;
-        load_x<T, NT, NC>(xrow, edge, kb * KB + t * 8, p.k, x);
-        load_scales<ZEROS>(p, sp, zp, srow, kb, sc);
-        if (ok) {
-          const bool got = mbar_wait_stage(&bar[used % STAGES], (used / STAGES) & 1u, s_abort, p.status, p.wait_ns);
-          ok = __all_sync(0xFFFFFFFFu, got);
-        }
-        if (ok) {
-          const uint32_t st = ring + (used % STAGES) * STAGE_BYTES;
-          chunks_mma<BF16, GS, ZEROS, NT, 0, NC>(st, acc, sc, x, lane, p.mask);
-          if constexpr (NT == 2) {
-            load_x<T, NT, NC>(xrow, edge, kb * KB + 64 + t * 8, p.k, x);
-            chunks_mma<BF16, GS, ZEROS, NT, 2, 2>(st, acc, sc, x, lane, p.mask);
-          }
-          ++used;
-          __syncwarp();   // every lane has read the stage
-          issue();
-        }
+        for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.0f;
+    // x runs one half ahead of its use, the scales one stage
+    uint4 x[2][NT][4];
+    Scales<KB / GS> sc, sn;
+    const int hend = min(2 * kb1, (p.k + KH - 1) / KH);   // halves past the row's end hold nothing
+    auto ahead = [&](int hk, uint4 (&xx)[NT][4]) {
+      if (hk < hend) load_x<T, NT, 4>(xrow, (hk + 1) * KH > p.k, hk * KH + t * 8, p.k, xx);
+    };
+    if (kb0 < kb1) {
+      ahead(2 * kb0, x[0]);
+      load_scales<ZEROS>(p, sp, zp, srow, kb0, sn);
+    }
+    for (int kb = kb0; kb < kb1; ++kb) {
+      ahead(2 * kb + 1, x[1]);
+      sc = sn;
+      if (kb + 1 < kb1) load_scales<ZEROS>(p, sp, zp, srow, kb + 1, sn);
+      if (ok) {
+        const bool got = mbar_wait_stage(&bar[used % STAGES], (used / STAGES) & 1u, s_abort, p.status, p.wait_ns);
+        ok = __all_sync(0xFFFFFFFFu, got);
       }
-      // partial sums of the warps along the contraction, in warp order
+      const uint32_t st = ring + (used % STAGES) * STAGE_BYTES;
+      if (ok) half_mma<BF16, GS, ZEROS, NT, 0>(p, st, acc, sc, x[0], lane);
+      if (kb + 1 < kb1) ahead(2 * kb + 2, x[0]);
+      if (ok) {
+        if (2 * kb + 1 < hend) half_mma<BF16, GS, ZEROS, NT, 1>(p, st, acc, sc, x[1], lane);
+        ++used;
+        __syncwarp();   // every lane has read the stage
+        issue();
+      }
+    }
+    // partial sums of the warps along the contraction, in warp order; in
+    // halves of the warp's rows: m = 0 and 2 (in the gate/up form 16 gate rows
+    // and the up rows that go with them), then m = 1 and 3
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        float* mine = red + warp * (BOX_ROWS * 8);
+    for (int j = 0; j < NT; ++j) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          *reinterpret_cast<float2*>(mine + (m * 16 + g) * 8 + 2 * t) = make_float2(acc[m][j][0], acc[m][j][1]);
-          *reinterpret_cast<float2*>(mine + (m * 16 + g + 8) * 8 + 2 * t) = make_float2(acc[m][j][2], acc[m][j][3]);
+      for (int hh = 0; hh < 2; ++hh) {
+        float* mine = red + warp * (RED_ROWS * 8) + g * 8 + 2 * t;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const float(&c)[4] = acc[hh + 2 * v][j];
+          *reinterpret_cast<float2*>(mine + v * 128) = make_float2(c[0], c[1]);
+          *reinterpret_cast<float2*>(mine + v * 128 + 64) = make_float2(c[2], c[3]);
         }
         column_sync(nw, p.wk);
         const int nr = min(8, u.nr - 8 * j);
-        for (int e = kw * 32 + lane; e < wrows * nr; e += p.wk * 32) {
-          const int r = p.dual ? e >> 5 : e >> 6, cc = e & (wrows - 1);
-          if (nbase + cc < p.n) {
-            const float* src = red + nw * p.wk * (BOX_ROWS * 8) + cc * 8 + r;
+        const int half = wrows >> 1;   // output columns of this half: 16 or 32
+        for (int e = kw * 32 + lane; e < half * nr; e += p.wk * 32) {
+          const int r = p.dual ? e >> 4 : e >> 5, cc = e & (half - 1);
+          // weight row of cc: row cc of m = hh, or (plain form, cc >= 16) of m = hh + 2
+          const int col = nbase + hh * 16 + cc + (cc & 16);
+          if (col < p.n) {
+            const float* src = red + nw * p.wk * (RED_ROWS * 8) + cc * 8 + r;
             float a = 0.0f, b = 0.0f;
-            for (int q = 0; q < p.wk; ++q) a += src[q * (BOX_ROWS * 8)];
+            for (int q = 0; q < p.wk; ++q) a += src[q * (RED_ROWS * 8)];
             if (p.dual) {
-              for (int q = 0; q < p.wk; ++q) b += src[q * (BOX_ROWS * 8) + wrows * 8];
+              for (int q = 0; q < p.wk; ++q) b += src[q * (RED_ROWS * 8) + 128];
               a = a / (1.0f + expf(-a)) * b;
             }
-            store_y(p, size_t(u.r0 + 8 * j + r) * size_t(p.ldy) + size_t(nbase + cc), a);
+            store_y(p, size_t(u.r0 + 8 * j + r) * size_t(p.ldy) + size_t(col), a);
           }
         }
         column_sync(nw, p.wk);   // the partial sums are rewritten
       }
-    };
-    if (u.nr > 8)
-      tile(std::integral_constant<int, 2>());
-    else
-      tile(std::integral_constant<int, 1>());
+    }
   }
   // copies issued but never used (only after an abort) must land first
   if (lane == 0) {
@@ -448,12 +546,12 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
 }
 
-template <bool BF16, int GS, bool ZEROS>
+template <bool BF16, int GS, bool ZEROS, int NT>
 cudaError_t launch(const moe_layer_s* L, const CUtensorMap& tm0, const CUtensorMap& tm1, W4Args a, long long units,
                    cudaStream_t st) {
   static std::atomic<bool> configured[kMaxDevices];   // the attribute is per device
   cudaError_t ce = once_per_device(configured, []() {
-    return cudaFuncSetAttribute(w4_kernel<BF16, GS, ZEROS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_DYN);
+    return cudaFuncSetAttribute(w4_kernel<BF16, GS, ZEROS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_DYN);
   });
   if (ce != cudaSuccess) return ce;
   a.wait_ns = kWaitLimitNs;
@@ -462,17 +560,27 @@ cudaError_t launch(const moe_layer_s* L, const CUtensorMap& tm0, const CUtensorM
     a.withhold = 1;
     L->test_stall_ns = 0;
   }
-  const long long cap = 2ll * L->num_sms;
+  const long long cap = static_cast<long long>(CTAS_PER_SM) * L->num_sms;
   const dim3 grid(unsigned(units < cap ? units : cap));
-  return launch_pdl(w4_kernel<BF16, GS, ZEROS>, grid, dim3(THREADS), SMEM_DYN, st, tm0, tm1, a);
+  return launch_pdl(w4_kernel<BF16, GS, ZEROS, NT>, grid, dim3(THREADS), SMEM_DYN, st, tm0, tm1, a);
 }
 
-template <bool BF16, bool ZEROS>
+template <bool BF16, bool ZEROS, int NT>
 cudaError_t launch_group(const moe_layer_s* L, int group, const CUtensorMap& tm0, const CUtensorMap& tm1,
                          const W4Args& a, long long units, cudaStream_t st) {
-  if (group == 32) return launch<BF16, 32, ZEROS>(L, tm0, tm1, a, units, st);
-  if (group == 64) return launch<BF16, 64, ZEROS>(L, tm0, tm1, a, units, st);
-  return launch<BF16, 128, ZEROS>(L, tm0, tm1, a, units, st);
+  if (group == 32) return launch<BF16, 32, ZEROS, NT>(L, tm0, tm1, a, units, st);
+  if (group == 64) return launch<BF16, 64, ZEROS, NT>(L, tm0, tm1, a, units, st);
+  return launch<BF16, 128, ZEROS, NT>(L, tm0, tm1, a, units, st);
+}
+
+template <int NT>
+cudaError_t launch_type(const moe_layer_s* L, moe_dtype t, bool zeros, int group, const CUtensorMap& tm0,
+                        const CUtensorMap& tm1, const W4Args& a, long long units, cudaStream_t st) {
+  if (t == MOE_BF16)
+    return zeros ? launch_group<true, true, NT>(L, group, tm0, tm1, a, units, st)
+                 : launch_group<true, false, NT>(L, group, tm0, tm1, a, units, st);
+  return zeros ? launch_group<false, true, NT>(L, group, tm0, tm1, a, units, st)
+               : launch_group<false, false, NT>(L, group, tm0, tm1, a, units, st);
 }
 
 }  // namespace
@@ -499,18 +607,27 @@ cudaError_t launch_w4(const moe_layer_s* L, moe_dtype t, const void* x, int x_ro
   p.k = k;
   p.ng = (k + w->group - 1) / w->group;
   p.dual = up != nullptr;
+  const int gps = KB / w->group;
+  p.vec = w->scale_type != MOE_F32 && p.ng % gps == 0;
+  for (int i = 0; i < 2; ++i)
+    p.vec = p.vec && reinterpret_cast<uintptr_t>(p.scales[i]) % (2 * gps) == 0 &&
+            reinterpret_cast<uintptr_t>(p.zeros[i]) % gps == 0;
   p.nkb = (k + KB - 1) / KB;
+  // Rows of a unit: 8, or 16 when groups hold more than 8 on average (the
+  // codes are then unpacked half as often, on two thirds of the warps).
+  const int nt = rows > 8ll * G ? 2 : 1;
   // Warps along the contraction. More of them give more, smaller units (the
   // only way to fill the machine with few experts), fewer leave more blocks
   // per unit to pay for its fixed cost (finding it, joining the partial sums:
   // about one block's time). The split with the shortest longest CTA:
-  const long long groups = rows / RMAX + (rows < G ? rows : G);   // units per column tile, at most
+  // units per column tile, at most
+  const long long groups = rows / (8 * nt) + (rows < G ? rows : G);
+  const long long ctas = static_cast<long long>(CTAS_PER_SM) * L->num_sms;
   long long best = 0;
   for (int wk = WARPS; wk >= 1; wk /= 2) {
     const int cols = (WARPS / wk) * (p.dual ? BOX_ROWS / 2 : BOX_ROWS);
     const long long units = groups * ((n + cols - 1) / cols);
-    const long long rounds = (units + 2 * L->num_sms - 1) / (2 * L->num_sms);
-    const long long cost = rounds * ((p.nkb + wk - 1) / wk + 1);
+    const long long cost = ((units + ctas - 1) / ctas) * (2 * ((p.nkb + wk - 1) / wk) + 1);
     if (best == 0 || cost < best) {
       best = cost;
       p.wk = wk;
@@ -529,11 +646,8 @@ cudaError_t launch_w4(const moe_layer_s* L, moe_dtype t, const void* x, int x_ro
   tm1 = tm0;
   if (up && !encode_tmap_codes(&tm1, up->codes, (k + 1) / 2, n, G, up->ld, box)) return cudaErrorInvalidValue;
   const long long units = groups * p.ntn;
-  if (t == MOE_BF16)
-    return w->zeros ? launch_group<true, true>(L, w->group, tm0, tm1, p, units, st)
-                    : launch_group<true, false>(L, w->group, tm0, tm1, p, units, st);
-  return w->zeros ? launch_group<false, true>(L, w->group, tm0, tm1, p, units, st)
-                  : launch_group<false, false>(L, w->group, tm0, tm1, p, units, st);
+  return nt == 1 ? launch_type<1>(L, t, w->zeros != nullptr, w->group, tm0, tm1, p, units, st)
+                 : launch_type<2>(L, t, w->zeros != nullptr, w->group, tm0, tm1, p, units, st);
 }
 
 }  // namespace moe
