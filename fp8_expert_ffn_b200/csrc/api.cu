@@ -89,6 +89,23 @@ bool encode_tmap_16(CUtensorMap* tm, moe_dtype t, const void* base, uint64_t inn
   return r == CUDA_SUCCESS;
 }
 
+bool encode_tmap_out(CUtensorMap* tm, moe_dtype t, void* base, uint64_t inner, uint64_t rows, uint64_t depth,
+                     uint64_t ld, uint32_t box_inner, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const uint64_t es = t == MOE_F32 ? 4 : 2;
+  cuuint64_t dims[3] = {inner, rows, depth};
+  cuuint64_t strides[2] = {ld * es, rows * ld * es};
+  cuuint32_t box[3] = {box_inner, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType dt = t == MOE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : t == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUresult r = fn(tm, dt, depth ? 3u : 2u, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 bool encode_tmap_codes(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t rows, uint64_t depth, uint64_t ld,
                        uint32_t box_rows) {
   EncodeTiledFn fn = encode_fn();

@@ -59,7 +59,8 @@ constexpr int FIRST_EPI_WARP = 4;
 constexpr int EPI_WARPS = 4;
 constexpr int RCHUNK = 8;               // row tiles per chunk of the tile order
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int SMEM_DYN = STAGES * STAGE_BYTES + 1024;
+constexpr int STG_BYTES = 8192;         // one staged chunk of output rows: 32 rows x 128 columns of 16 bits, or 16 of fp32
+constexpr int SMEM_DYN = STAGES * STAGE_BYTES + 2 * STG_BYTES + 1024;
 
 struct GmmArgs {
   const int32_t* offsets;   // [ngroups + 1]
@@ -72,6 +73,9 @@ struct GmmArgs {
   long long ld;             // output row stride, elements
   int out_type;             // moe_dtype
   int accumulate;           // wgrad: add to what `out` holds
+  int bulk;                 // the output takes bulk tensor stores (aligned base and stride),
+  int bulk_edge;            // also of boxes that reach past its last column: they write whole
+                            // 16-byte pieces, so its rows have to end with one
   uint32_t idesc;           // instruction descriptor without N
   uint32_t* status;
   unsigned long long wait_ns;
@@ -161,9 +165,24 @@ __device__ __forceinline__ void store_chunk(const GmmArgs& p, size_t at, const f
     store_rows(static_cast<__half*>(p.out) + at, p.ld, v, m, p.accumulate);
 }
 
+// Whether `ok` holds in every thread of the four epilogue warps (a barrier).
+__device__ __forceinline__ bool epilogue_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "barrier.cta.red.and.pred p, 1, 128, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(uint32_t(ok))
+      : "memory");
+  return r != 0;
+}
+
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    grouped_mm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ RowMaps tmB, const GmmArgs p) {
+    grouped_mm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ RowMaps tmB,
+                      const __grid_constant__ CUtensorMap tmO, const GmmArgs p) {
   constexpr bool A_MN = MODE != MOE_MM_FORWARD;   // A's contraction is its slow dimension
   constexpr bool B_MN = MODE == MOE_MM_WGRAD;
   extern __shared__ uint8_t smem_raw[];
@@ -346,7 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else if (warp >= FIRST_EPI_WARP) {
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3;   // TMEM lane quarter this warp may access
-    uint32_t tb = 0;
+    uint32_t tb = 0, sb = 0;
     for (int i = pair; i < total; i += npairs) {
       const Tile t = decode_tile<MODE>(i, s_plan, p);
       const int col = t.col0 + int(rank) * 128 + q * 32 + lane;
@@ -364,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       const uint32_t buf = tb & 1u;
       const bool got = mbar_wait_stage(&tfull_bar[buf], (tb >> 1) & 1u, s_abort, p.status, p.wait_ns);
-      if (!__all_sync(0xFFFFFFFFu, got)) break;
+      if (!epilogue_all(got)) break;   // all four warps leave together: they share barriers below
       tc_fence_after();
       const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + buf * BR;
       for (int c = 0; c < t.nrows; c += 32) {
@@ -376,10 +395,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_rank(&tempty_bar[buf], 0);
         }
-        if (cv) store_chunk(p, at + size_t(c) * size_t(p.ld), v, min(32, t.nrows - c));
+        const int m = min(32, t.nrows - c);
+        // Bulk stores for whole chunks; a ragged group's last rows are stored
+        // one by one, so that no row behind them is touched (a weight's last
+        // rows are cut off by the tensor map).
+        const int x = t.col0 + int(rank) * 128;
+        if (p.bulk && (MODE == MOE_MM_WGRAD || m == 32) && (p.bulk_edge || x + 128 <= p.nc)) {
+          const int parts = p.out_type == MOE_F32 ? 2 : 1;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == parts) break;
+            // one thread issues all stores: its last but one has read the
+            // buffer that is written now
+            if (warp == FIRST_EPI_WARP && lane == 0) bulk_wait_read1();
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            uint8_t* stg = smem + STAGES * STAGE_BYTES + (sb & 1u) * STG_BYTES;
+            if (p.out_type == MOE_F32) {
+              float* o = reinterpret_cast<float*>(stg) + q * 32 + lane;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j * 128] = v[16 * h + j];
+            } else if (p.out_type == MOE_BF16) {
+              __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(stg) + q * 32 + lane;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j * 128] = __float2bfloat16_rn(v[j]);
+            } else {
+              __half* o = reinterpret_cast<__half*>(stg) + q * 32 + lane;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j * 128] = __float2half_rn(v[j]);
+            }
+            fence_proxy_async_smem();
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (warp == FIRST_EPI_WARP && lane == 0) {
+              const int y = t.row0 + c + 16 * h;
+              if (MODE == MOE_MM_WGRAD) {
+                if (x < p.nc && y < p.nr) {
+                  if (p.accumulate)
+                    tma_add_3d(&tmO, stg, x, y, t.g);
+                  else
+                    tma_store_3d(&tmO, stg, x, y, t.g);
+                }
+              } else if (x < p.nc) {
+                tma_store_2d(&tmO, stg, x, y);
+              }
+              bulk_commit();
+            }
+            ++sb;
+          }
+        } else if (cv) {
+          store_chunk(p, at + size_t(c) * size_t(p.ld), v, m);
+        }
       }
       ++tb;
     }
+    if (warp == FIRST_EPI_WARP && lane == 0) bulk_wait0();   // stores complete before the CTA exits
   }
   // ------------------------------------------------------------------ teardown
   __syncthreads();
@@ -403,6 +471,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 template <int MODE>
 cudaError_t launch_mode(const moe_layer_s* L, const CUtensorMap& tmA, const RowMaps& tmB, GmmArgs a, long long tiles,
                         cudaStream_t st) {
+  // bulk stores want the base and the row stride in 16-byte units; 16-bit
+  // accumulation rounds once, which a bulk add to the 16-bit values would not
+  const int es = a.out_type == MOE_F32 ? 4 : 2;
+  CUtensorMap tmO = tmA;
+  a.bulk = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.ld * es % 16 == 0 && !(a.accumulate && es == 2);
+  a.bulk_edge = a.nc * es % 16 == 0;
+  if (a.bulk && !encode_tmap_out(&tmO, static_cast<moe_dtype>(a.out_type), a.out, a.nc,
+                                 MODE == MOE_MM_WGRAD ? a.nr : a.rows, MODE == MOE_MM_WGRAD ? a.nweights : 0, a.ld,
+                                 128, STG_BYTES / 128 / es))
+    return cudaErrorInvalidValue;
   static std::atomic<bool> configured[kMaxDevices];   // the attribute is per device
   cudaError_t ce = once_per_device(configured, []() {
     return cudaFuncSetAttribute(grouped_mm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_DYN);
@@ -416,7 +494,7 @@ cudaError_t launch_mode(const moe_layer_s* L, const CUtensorMap& tmA, const RowM
   }
   const long long pairs = tiles < L->num_sms / 2 ? tiles : L->num_sms / 2;
   if (pairs <= 0) return cudaSuccess;
-  return launch_pdl(grouped_mm_kernel<MODE>, dim3(unsigned(2 * pairs)), dim3(THREADS), SMEM_DYN, st, tmA, tmB, a);
+  return launch_pdl(grouped_mm_kernel<MODE>, dim3(unsigned(2 * pairs)), dim3(THREADS), SMEM_DYN, st, tmA, tmB, tmO, a);
 }
 
 // A row operand [rows][cols] whose rows are the tile's N (K-major boxes).

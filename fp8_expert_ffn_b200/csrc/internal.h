@@ -188,6 +188,10 @@ bool encode_tmap(CUtensorMap* tm, bool bf16, const void* base, uint64_t inner, u
 // elements, 128-byte swizzle; elements past the extents read as zero.
 bool encode_tmap_16(CUtensorMap* tm, moe_dtype t, const void* base, uint64_t inner, uint64_t rows, uint64_t depth,
                     uint64_t ld, uint32_t box_inner, uint32_t box_rows);
+// Map of an output [depth][rows][inner] (depth 0: 2-D) of any moe_dtype for
+// bulk stores from unswizzled boxes.
+bool encode_tmap_out(CUtensorMap* tm, moe_dtype t, void* base, uint64_t inner, uint64_t rows, uint64_t depth,
+                     uint64_t ld, uint32_t box_inner, uint32_t box_rows);
 // Map of 4-bit codes [depth][rows][inner bytes], row stride `ld` bytes, boxes
 // of box_rows x 128 bytes with 128-byte swizzle.
 bool encode_tmap_codes(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t rows, uint64_t depth, uint64_t ld,
