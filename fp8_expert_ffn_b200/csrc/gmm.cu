@@ -345,12 +345,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             // rows [left, 64) of every box belong to the next group (or lie
             // past the last row): set them to zero
             const int boxes = 2 + ((tile_n(t) / 2 + 63) >> 6);
-            const int vecs = (BK - left) * 8;   // 16-byte pieces per box
-            for (int v = lane; v < boxes * vecs; v += 32) {
-              const int bx = v / vecs;
-              *reinterpret_cast<uint4*>(smem + s * STAGE_BYTES + bx * BOX_BYTES + left * 128 + (v - bx * vecs) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
+            uint8_t* first = smem + s * STAGE_BYTES + lane * 16;   // four 128-byte rows per warp store
+            for (int bx = 0; bx < boxes; ++bx)
+              for (int r = left * 128; r < BOX_BYTES - lane * 16; r += 512)
+                *reinterpret_cast<uint4*>(first + bx * BOX_BYTES + r) = make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
             __syncwarp();
             cluster_fence();   // the leading CTA's MMAs read these zeros

@@ -158,17 +158,19 @@ MM_SHAPES = [
 ]
 
 
+@pytest.mark.parametrize("aligned", [False, True])   # output rows of any stride, or of 16-byte pieces
 @pytest.mark.parametrize("dt,out_dt", [(BF, BF), (HF, F32), (HF, HF), (BF, F32)])
 @pytest.mark.parametrize("op", OPS)
 @pytest.mark.parametrize("shape", MM_SHAPES, ids=str)
-def test_mm_exact_integers(shape, op, dt, out_dt):
+def test_mm_exact_integers(shape, op, dt, out_dt, aligned):
     counts, S, n, k = shape
     rng = np.random.default_rng(n * 1000 + k)
     gr = Groups(counts, S, lead=3, tail=5)
     x = ints(rng, (gr.rows, k), 4) if op != "dgrad" else None
     dy = ints(rng, (gr.rows, n), 4) if op != "mm" else None
     w = ints(rng, (gr.G, n, k), 4) if op != "wgrad" else None
-    res = run_mm(op, gr, dt, out_dt, n, k, x, dy, w)
+    cols = n if op == "mm" else k
+    res = run_mm(op, gr, dt, out_dt, n, k, x, dy, w, ldo_extra=up8(cols, 8) - cols if aligned else 3)
     ref, _ = mm_reference(op, gr, x, dy, w)
     if op != "wgrad":
         res, ref = res[gr.first:gr.last], ref[gr.first:gr.last]
@@ -196,7 +198,8 @@ def test_mm_random(counts, S, n, k, op, dt, out_dt):
     x = normal(rng, (gr.rows, k)).to(dt).double() if op != "dgrad" else None
     dy = normal(rng, (gr.rows, n), 0.1).to(dt).double() if op != "mm" else None
     w = normal(rng, (gr.G, n, k), k ** -0.5).to(dt).double() if op != "wgrad" else None
-    res = run_mm(op, gr, dt, out_dt, n, k, x, dy, w)
+    cols = n if op == "mm" else k
+    res = run_mm(op, gr, dt, out_dt, n, k, x, dy, w, ldo_extra=up8(cols) - cols)
     ref, mag = mm_reference(op, gr, x, dy, w)
     if op != "wgrad":
         res, ref, mag = res[:gr.last], ref[:gr.last], mag[:gr.last]
@@ -204,14 +207,15 @@ def test_mm_random(counts, S, n, k, op, dt, out_dt):
     check_bound(res, ref, mag, terms, out_dt, op)
 
 
+@pytest.mark.parametrize("aligned", [False, True])
 @pytest.mark.parametrize("out_dt", [BF, F32])
-def test_wgrad_accumulates(out_dt):
+def test_wgrad_accumulates(out_dt, aligned):
     rng = np.random.default_rng(5)
     gr = Groups((40, 0, 100), 0, tail=2)
     n, k = 70, 300
     x, dy = ints(rng, (gr.rows, k), 3), ints(rng, (gr.rows, n), 3)
     old = ints(rng, (gr.G, n, k), 100)
-    res = run_mm("wgrad", gr, BF, out_dt, n, k, x, dy, None, accumulate=old)
+    res = run_mm("wgrad", gr, BF, out_dt, n, k, x, dy, None, ldo_extra=8 - k % 8 if aligned else 3, accumulate=old)
     ref, _ = mm_reference("wgrad", gr, x, dy, None)
     assert torch.equal(res, (ref + old).to(F32).to(out_dt))
 
