@@ -24,7 +24,7 @@
 // Each CTA holds its own 128 columns of A and half of B's rows, so a
 // 256 x 256 tile moves 32 KB per CTA and 64-deep K block from L2 where two
 // independent 128 x 256 tiles would move 48 KB.
-//   warp 0      TMA producer into a 6-stage ring (16 KB of A, up to 16 KB of B)
+//   warp 0      TMA producer into a ring of 6 stages (16 KB of A, up to 16 KB of B)
 //   warp 1      TMEM allocation; in the leading CTA the MMA issuer
 //   warp 2      relay: waits for its CTA's copies, zeroes a wgrad tail, and
 //               signals the leading CTA
@@ -47,12 +47,8 @@ namespace moe {
 namespace {
 
 constexpr int BC = 256;                 // output columns per tile (128 per CTA)
-constexpr int BR = 256;                 // output rows per tile, at most
 constexpr int BK = 64;                  // contraction per stage (128 bytes)
-constexpr int STAGES = 6;
 constexpr int A_BYTES = 128 * BK * 2;   // 16 KB
-constexpr int B_BYTES = 128 * BK * 2;
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int BOX_BYTES = 64 * 64 * 2;  // one MN-major box: 64 contraction rows x 64 columns
 constexpr int THREADS = 256;
 constexpr int FIRST_EPI_WARP = 4;
@@ -60,7 +56,15 @@ constexpr int EPI_WARPS = 4;
 constexpr int RCHUNK = 8;               // row tiles per chunk of the tile order
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int STG_BYTES = 8192;         // one staged chunk of output rows: 32 rows x 128 columns of 16 bits, or 16 of fp32
-constexpr int SMEM_DYN = STAGES * STAGE_BYTES + 2 * STG_BYTES + 1024;
+constexpr int TMEM_BUF = 256;           // TMEM columns of one of the two accumulators
+
+// BR: output rows per tile, at most. 256 fill the MMA; 64 are for a few rows
+// per group, where the stages hold little but weights and more of them can be
+// on their way (10 stages of 20 KB instead of 6 of 32 KB: one decode step of
+// 65 experts, 1 GB of weights, 190 -> 175 us).
+constexpr int stage_bytes(int BR) { return A_BYTES + BR * BK; }   // each CTA holds half of the rows
+constexpr int stages(int BR) { return BR == 64 ? 10 : 6; }
+constexpr int smem_dyn(int BR) { return stages(BR) * stage_bytes(BR) + 2 * STG_BYTES + 1024; }
 
 struct GmmArgs {
   const int32_t* offsets;   // [ngroups + 1]
@@ -94,7 +98,7 @@ struct Tile {
   // weight for wgrad); nrows: valid rows; r_first, wgrad: the group's first row
 };
 
-template <int MODE>
+template <int MODE, int BR>
 __device__ __forceinline__ Tile decode_tile(int i, const GroupPlan& s, const GmmArgs& p) {
   Tile t;
   t.g = find_group(s.prefix, p.ngroups, i);
@@ -179,12 +183,13 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
   return r != 0;
 }
 
-template <int MODE>
+template <int MODE, int BR>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     grouped_mm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ RowMaps tmB,
                       const __grid_constant__ CUtensorMap tmO, const GmmArgs p) {
   constexpr bool A_MN = MODE != MOE_MM_FORWARD;   // A's contraction is its slow dimension
   constexpr bool B_MN = MODE == MOE_MM_WGRAD;
+  constexpr int STAGES = stages(BR), STAGE_BYTES = stage_bytes(BR);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[STAGES];    // this CTA's copies of a stage
   __shared__ __align__(8) uint64_t ready_bar[STAGES];   // leading CTA: both CTAs' stages complete
@@ -248,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       uint32_t it = 0;
       bool ok = true;
       for (int i = pair; ok && i < total; i += npairs) {
-        const Tile t = decode_tile<MODE>(i, s_plan, p);
+        const Tile t = decode_tile<MODE, BR>(i, s_plan, p);
         const int half = tile_n(t) >> 1;
         const int acol = t.col0 + int(rank) * 128;
         const int brow = t.row0 + int(rank) * half;
@@ -297,12 +302,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       uint32_t it = 0, tb = 0;
       bool ok = true;
       for (int i = pair; ok && i < total; i += npairs) {
-        const Tile t = decode_tile<MODE>(i, s_plan, p);
+        const Tile t = decode_tile<MODE, BR>(i, s_plan, p);
         if (t.nk == 0) continue;
         const uint32_t idesc = p.idesc | (uint32_t(tile_n(t) >> 3) << 17);
         const uint32_t buf = tb & 1u;
         if (!mbar_wait_stage(&tempty_bar[buf], ((tb >> 1) & 1u) ^ 1u, s_abort, p.status, p.wait_ns)) break;
-        const uint32_t d = tmem_base + buf * BR;
+        const uint32_t d = tmem_base + buf * TMEM_BUF;
         for (int kb = 0; kb < t.nk; ++kb) {
           const int s = it % STAGES;
           if (!mbar_wait_stage(&ready_bar[s], (it / STAGES) & 1u, s_abort, p.status, p.wait_ns)) { ok = false; break; }
@@ -333,7 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint32_t it = 0;
     bool ok = true;
     for (int i = pair; ok && i < total; i += npairs) {
-      const Tile t = decode_tile<MODE>(i, s_plan, p);
+      const Tile t = decode_tile<MODE, BR>(i, s_plan, p);
       int left = 0;   // wgrad: the group's rows from the current block on
       if (MODE == MOE_MM_WGRAD) left = s_plan.off[t.g + 1] - t.r_first;
       for (int kb = 0; kb < t.nk; ++kb) {
@@ -365,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int q = warp & 3;   // TMEM lane quarter this warp may access
     uint32_t tb = 0, sb = 0;
     for (int i = pair; i < total; i += npairs) {
-      const Tile t = decode_tile<MODE>(i, s_plan, p);
+      const Tile t = decode_tile<MODE, BR>(i, s_plan, p);
       const int col = t.col0 + int(rank) * 128 + q * 32 + lane;
       const bool cv = col < p.nc;
       size_t at = size_t(t.row0) * size_t(p.ld) + size_t(col);
@@ -383,7 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const bool got = mbar_wait_stage(&tfull_bar[buf], (tb >> 1) & 1u, s_abort, p.status, p.wait_ns);
       if (!epilogue_all(got)) break;   // all four warps leave together: they share barriers below
       tc_fence_after();
-      const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + buf * BR;
+      const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + buf * TMEM_BUF;
       for (int c = 0; c < t.nrows; c += 32) {
         float v[32];
         tmem_ld32(tbase + uint32_t(c), v);
@@ -466,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync();
 }
 
-template <int MODE>
+template <int MODE, int BR>
 cudaError_t launch_mode(const moe_layer_s* L, const CUtensorMap& tmA, const RowMaps& tmB, GmmArgs a, long long tiles,
                         cudaStream_t st) {
   // bulk stores want the base and the row stride in 16-byte units; 16-bit
@@ -481,7 +486,7 @@ cudaError_t launch_mode(const moe_layer_s* L, const CUtensorMap& tmA, const RowM
     return cudaErrorInvalidValue;
   static std::atomic<bool> configured[kMaxDevices];   // the attribute is per device
   cudaError_t ce = once_per_device(configured, []() {
-    return cudaFuncSetAttribute(grouped_mm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_DYN);
+    return cudaFuncSetAttribute(grouped_mm_kernel<MODE, BR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_dyn(BR));
   });
   if (ce != cudaSuccess) return ce;
   a.wait_ns = kWaitLimitNs;
@@ -492,7 +497,7 @@ cudaError_t launch_mode(const moe_layer_s* L, const CUtensorMap& tmA, const RowM
   }
   const long long pairs = tiles < L->num_sms / 2 ? tiles : L->num_sms / 2;
   if (pairs <= 0) return cudaSuccess;
-  return launch_pdl(grouped_mm_kernel<MODE>, dim3(unsigned(2 * pairs)), dim3(THREADS), SMEM_DYN, st, tmA, tmB, tmO, a);
+  return launch_pdl(grouped_mm_kernel<MODE, BR>, dim3(unsigned(2 * pairs)), dim3(THREADS), smem_dyn(BR), st, tmA, tmB, tmO, a);
 }
 
 // A row operand [rows][cols] whose rows are the tile's N (K-major boxes).
@@ -529,7 +534,7 @@ cudaError_t launch_grouped_mm(const moe_layer_s* L, int mode, moe_dtype t, const
     if (!encode_tmap_16(&tmA, t, b, k, rows, 0, ldb, 64, 64) || !encode_tmap_16(&tmB.m[0], t, a, n, rows, 0, lda, 64, 64))
       return cudaErrorInvalidValue;
     for (int j = 1; j < 4; ++j) tmB.m[j] = tmB.m[0];
-    return launch_mode<MOE_MM_WGRAD>(L, tmA, tmB, p, static_cast<long long>(G) * ((n + BR - 1) / BR) * p.ntc, st);
+    return launch_mode<MOE_MM_WGRAD, 256>(L, tmA, tmB, p, static_cast<long long>(G) * ((n + 255) / 256) * p.ntc, st);
   }
   // a = the rows, b = w [G][n][k]
   const int contraction = mode == MOE_MM_FORWARD ? k : n;
@@ -539,10 +544,15 @@ cudaError_t launch_grouped_mm(const moe_layer_s* L, int mode, moe_dtype t, const
   if (!encode_tmap_16(&tmA, t, b, k, n, G, ldb, 64, mode == MOE_MM_FORWARD ? 128 : 64) ||
       !encode_row_maps(&tmB, t, a, contraction, rows, lda))
     return cudaErrorInvalidValue;
+  // few rows per group on average: narrow tiles (larger groups take several)
+  const int br = rows <= 32ll * G ? 64 : 256;
   // upper bound on the tiles: every group may add one partial row tile
-  const long long tiles = (static_cast<long long>(rows) / BR + (rows < G ? rows : G)) * p.ntc;
-  if (mode == MOE_MM_FORWARD) return launch_mode<MOE_MM_FORWARD>(L, tmA, tmB, p, tiles, st);
-  return launch_mode<MOE_MM_DGRAD>(L, tmA, tmB, p, tiles, st);
+  const long long tiles = (static_cast<long long>(rows) / br + (rows < G ? rows : G)) * p.ntc;
+  if (mode == MOE_MM_FORWARD)
+    return br == 64 ? launch_mode<MOE_MM_FORWARD, 64>(L, tmA, tmB, p, tiles, st)
+                    : launch_mode<MOE_MM_FORWARD, 256>(L, tmA, tmB, p, tiles, st);
+  return br == 64 ? launch_mode<MOE_MM_DGRAD, 64>(L, tmA, tmB, p, tiles, st)
+                  : launch_mode<MOE_MM_DGRAD, 256>(L, tmA, tmB, p, tiles, st);
 }
 
 }  // namespace moe
