@@ -29,7 +29,7 @@
 //   warp 2      relay: waits for its CTA's copies, zeroes a wgrad tail, and
 //               signals the leading CTA
 //   warp 3      idle
-//   warps 4-7   epilogue: TMEM lanes 32*(w%4).., one output column per lane;
+//   warps 4-    epilogue (4 warps, 8 where it adds parts of a sum): TMEM lanes 32*(w%4).., one output column per lane;
 //               two 256-column TMEM buffers overlap it with the next tile
 // No TMA multicast; commits signal both CTAs. Every wait is bounded (1 s): on
 // a timeout the status word is set, all roles leave, copies in flight are
@@ -50,9 +50,7 @@ constexpr int BC = 256;                 // output columns per tile (128 per CTA)
 constexpr int BK = 64;                  // contraction per stage (128 bytes)
 constexpr int A_BYTES = 128 * BK * 2;   // 16 KB
 constexpr int BOX_BYTES = 64 * 64 * 2;  // one MN-major box: 64 contraction rows x 64 columns
-constexpr int THREADS = 256;
 constexpr int FIRST_EPI_WARP = 4;
-constexpr int EPI_WARPS = 4;
 constexpr int RCHUNK = 8;               // row tiles per chunk of the tile order
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int STG_BYTES = 8192;         // one staged chunk of output rows: 32 rows x 128 columns of 16 bits, or 16 of fp32
@@ -63,8 +61,26 @@ constexpr int TMEM_BUF = 256;           // TMEM columns of one of the two accumu
 // on their way (10 stages of 20 KB instead of 6 of 32 KB: one decode step of
 // 65 experts, 1 GB of weights, 190 -> 175 us).
 constexpr int stage_bytes(int BR) { return A_BYTES + BR * BK; }   // each CTA holds half of the rows
-constexpr int stages(int BR) { return BR == 64 ? 10 : 6; }
-constexpr int smem_dyn(int BR) { return stages(BR) * stage_bytes(BR) + 2 * STG_BYTES + 1024; }
+
+// PROMOTE: fp32 outputs over a long contraction. The MMA adds to its fp32
+// accumulator by truncation, so a sum's error grows with the number of its
+// additions (2.3e-6 of the result after 2,600 terms, twenty times that of an
+// fp32 product). These tiles hand the accumulator over every SEGMENT K blocks
+// (512 terms) and the epilogue adds the parts in registers, rounding to
+// nearest: 8 warps with 128 rows of a column each, their registers taken from
+// the other warps as in the FP8 GEMMs. 16-bit outputs, whose rounding is a
+// thousand times larger, keep one sum.
+constexpr int SEGMENT = 8;
+constexpr int epi_warps(bool promote) { return promote ? 8 : 4; }
+constexpr int threads(bool promote) { return 32 * (FIRST_EPI_WARP + epi_warps(promote)); }
+constexpr int stages(int BR, bool promote) { return (BR == 64 ? 10 : 6) - (promote ? 1 : 0); }
+constexpr int smem_dyn(int BR, bool promote) {
+  return stages(BR, promote) * stage_bytes(BR) + epi_warps(promote) / 2 * STG_BYTES + 1024;
+}
+constexpr int LAUNCH_REGS = 168;     // 384 threads, one CTA per SM
+constexpr int PRODUCER_REGS = 40;
+constexpr int EPILOGUE_REGS = 232;
+static_assert(128 * PRODUCER_REGS + 256 * EPILOGUE_REGS <= 384 * LAUNCH_REGS, "register split exceeds launch");
 
 struct GmmArgs {
   const int32_t* offsets;   // [ngroups + 1]
@@ -169,27 +185,32 @@ __device__ __forceinline__ void store_chunk(const GmmArgs& p, size_t at, const f
     store_rows(static_cast<__half*>(p.out) + at, p.ld, v, m, p.accumulate);
 }
 
-// Whether `ok` holds in every thread of the four epilogue warps (a barrier).
-__device__ __forceinline__ bool epilogue_all(bool ok) {
+// Barrier of the four warps of epilogue warpgroup wg, and whether `ok` holds
+// in every thread of them (a barrier too).
+__device__ __forceinline__ void epilogue_sync(int wg) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
+}
+__device__ __forceinline__ bool epilogue_all(int wg, bool ok) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 q, %1, 0;\n\t"
-      "barrier.cta.red.and.pred p, 1, 128, q;\n\t"
+      "barrier.cta.red.and.pred p, %2, 128, q;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(r)
-      : "r"(uint32_t(ok))
+      : "r"(uint32_t(ok)), "r"(1 + wg)
       : "memory");
   return r != 0;
 }
 
-template <int MODE, int BR>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+template <int MODE, int BR, bool PROMOTE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
     grouped_mm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ RowMaps tmB,
                       const __grid_constant__ CUtensorMap tmO, const GmmArgs p) {
   constexpr bool A_MN = MODE != MOE_MM_FORWARD;   // A's contraction is its slow dimension
   constexpr bool B_MN = MODE == MOE_MM_WGRAD;
-  constexpr int STAGES = stages(BR), STAGE_BYTES = stage_bytes(BR);
+  constexpr int STAGES = stages(BR, PROMOTE), STAGE_BYTES = stage_bytes(BR);
+  constexpr int THREADS = threads(PROMOTE), EPI_WARPS = epi_warps(PROMOTE);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[STAGES];    // this CTA's copies of a stage
   __shared__ __align__(8) uint64_t ready_bar[STAGES];   // leading CTA: both CTAs' stages complete
@@ -247,6 +268,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_s;
 
+  if (warp < FIRST_EPI_WARP) {
+  if (PROMOTE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PRODUCER_REGS));
   if (warp == 0) {
     // -------------------------------------------------------------- producer
     if (elect_one()) {
@@ -305,10 +328,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const Tile t = decode_tile<MODE, BR>(i, s_plan, p);
         if (t.nk == 0) continue;
         const uint32_t idesc = p.idesc | (uint32_t(tile_n(t) >> 3) << 17);
-        const uint32_t buf = tb & 1u;
-        if (!mbar_wait_stage(&tempty_bar[buf], ((tb >> 1) & 1u) ^ 1u, s_abort, p.status, p.wait_ns)) break;
-        const uint32_t d = tmem_base + buf * TMEM_BUF;
         for (int kb = 0; kb < t.nk; ++kb) {
+          const int part = PROMOTE ? kb % SEGMENT : kb;   // K block within the accumulator's sum
+          const uint32_t buf = tb & 1u;
+          if (part == 0 &&
+              !mbar_wait_stage(&tempty_bar[buf], ((tb >> 1) & 1u) ^ 1u, s_abort, p.status, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          const uint32_t d = tmem_base + buf * TMEM_BUF;
           const int s = it % STAGES;
           if (!mbar_wait_stage(&ready_bar[s], (it / STAGES) & 1u, s_abort, p.status, p.wait_ns)) { ok = false; break; }
           if (MODE == MOE_MM_WGRAD && kb == t.nk - 1) cluster_fence();   // the relays' zeros
@@ -321,13 +349,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             // 16 of the contraction: 32 bytes along a K-major row, two 8-row
             // atoms (2048 bytes) of an MN-major box (address field in 16 bytes)
             mma_f16_pair(d, ad + uint64_t(k * (A_MN ? 128 : 2)), bd + uint64_t(k * (B_MN ? 128 : 2)), idesc,
-                         (kb | k) ? 1u : 0u);
+                         (part | k) ? 1u : 0u);
           tc_commit_pair(&empty_bar[s]);
           ++it;
+          if (kb == t.nk - 1 || (PROMOTE && part == SEGMENT - 1)) {
+            tc_commit_pair(&tfull_bar[buf]);
+            ++tb;
+          }
         }
-        if (!ok) break;
-        tc_commit_pair(&tfull_bar[buf]);
-        ++tb;
       }
       tc_commit_pair_self(&done_bar);   // all MMAs issued above have completed
       int never = 0;
@@ -365,54 +394,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
     }
     if (lane == 0) s_relayed = it;
-  } else if (warp >= FIRST_EPI_WARP) {
+  }
+  // ------------------------------------------------ teardown (warps 0 to 3)
+  __syncwarp();
+  asm volatile("bar.sync 0;" ::: "memory");
+  if (warp == 0 && lane == 0) {
+    // copies issued but never relayed (only after an abort) must land first
+    int never = 0;
+    for (uint32_t j = s_relayed; j < s_issued; ++j)
+      if (j != s_withheld) mbar_wait_stage(&full_bar[j % STAGES], (j / STAGES) & 1u, &never, p.status, p.wait_ns);
+  }
+  __syncwarp();
+  tc_fence_before();
+  asm volatile("bar.sync 0;" ::: "memory");
+  cluster_sync();   // both CTAs are past their last remote arrival and MMA
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+  cluster_sync();
+  } else {
     // -------------------------------------------------------------- epilogue
-    const int q = warp & 3;   // TMEM lane quarter this warp may access
+    // (its own copy of the teardown, so that both register limits hold on
+    // every instruction that they meet)
+    if (PROMOTE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPILOGUE_REGS));
+    const int q = warp & 3;                           // TMEM lane quarter this warp may access
+    const int wg = (warp - FIRST_EPI_WARP) >> 2;      // PROMOTE: the half of the rows
+    const bool storer = q == 0 && lane == 0;          // one thread per warpgroup issues the bulk stores
+    uint8_t* staging = smem + STAGES * STAGE_BYTES + wg * 2 * STG_BYTES;
     uint32_t tb = 0, sb = 0;
     for (int i = pair; i < total; i += npairs) {
       const Tile t = decode_tile<MODE, BR>(i, s_plan, p);
-      const int col = t.col0 + int(rank) * 128 + q * 32 + lane;
+      const int x = t.col0 + int(rank) * 128;
+      const int col = x + q * 32 + lane;
       const bool cv = col < p.nc;
       size_t at = size_t(t.row0) * size_t(p.ld) + size_t(col);
       if (MODE == MOE_MM_WGRAD) at += size_t(t.g) * size_t(p.nr) * size_t(p.ld);
-      if (t.nk == 0) {   // wgrad of a group without rows
-        if (!p.accumulate && cv) {
-          float z[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) z[j] = 0.0f;
-          for (int c = 0; c < t.nrows; c += 32) store_chunk(p, at + size_t(c) * size_t(p.ld), z, min(32, t.nrows - c));
-        }
-        continue;
-      }
-      const uint32_t buf = tb & 1u;
-      const bool got = mbar_wait_stage(&tfull_bar[buf], (tb >> 1) & 1u, s_abort, p.status, p.wait_ns);
-      if (!epilogue_all(got)) break;   // all four warps leave together: they share barriers below
-      tc_fence_after();
-      const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + buf * TMEM_BUF;
-      for (int c = 0; c < t.nrows; c += 32) {
-        float v[32];
-        tmem_ld32(tbase + uint32_t(c), v);
-        tmem_ld_wait();
-        if (c + 32 >= t.nrows) {   // the buffer is in registers: hand it back
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_rank(&tempty_bar[buf], 0);
-        }
+      // rows [c, c + 32) of the tile
+      auto put = [&](int c, const float (&v)[32]) {
         const int m = min(32, t.nrows - c);
         // Bulk stores for whole chunks; a ragged group's last rows are stored
         // one by one, so that no row behind them is touched (a weight's last
         // rows are cut off by the tensor map).
-        const int x = t.col0 + int(rank) * 128;
         if (p.bulk && (MODE == MOE_MM_WGRAD || m == 32) && (p.bulk_edge || x + 128 <= p.nc)) {
           const int parts = p.out_type == MOE_F32 ? 2 : 1;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (h == parts) break;
-            // one thread issues all stores: its last but one has read the
-            // buffer that is written now
-            if (warp == FIRST_EPI_WARP && lane == 0) bulk_wait_read1();
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            uint8_t* stg = smem + STAGES * STAGE_BYTES + (sb & 1u) * STG_BYTES;
+            // the last store but one has read the buffer that is written now
+            if (storer) bulk_wait_read1();
+            epilogue_sync(wg);
+            uint8_t* stg = staging + (sb & 1u) * STG_BYTES;
             if (p.out_type == MOE_F32) {
               float* o = reinterpret_cast<float*>(stg) + q * 32 + lane;
 #pragma unroll
@@ -427,8 +460,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               for (int j = 0; j < 32; ++j) o[j * 128] = __float2half_rn(v[j]);
             }
             fence_proxy_async_smem();
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (warp == FIRST_EPI_WARP && lane == 0) {
+            epilogue_sync(wg);
+            if (storer) {
               const int y = t.row0 + c + 16 * h;
               if (MODE == MOE_MM_WGRAD) {
                 if (x < p.nc && y < p.nr) {
@@ -447,32 +480,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         } else if (cv) {
           store_chunk(p, at + size_t(c) * size_t(p.ld), v, m);
         }
+      };
+      if (t.nk == 0) {   // wgrad of a group without rows
+        if (!p.accumulate && wg == 0) {
+          float z[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z[j] = 0.0f;
+          for (int c = 0; c < t.nrows; c += 32) put(c, z);
+        }
+        continue;
       }
-      ++tb;
+      // the accumulator of the tile's next part, or false: give up (all warps
+      // of the warpgroup together, since they share barriers)
+      auto accumulator = [&](uint32_t& tbase) {
+        const uint32_t buf = tb & 1u;
+        const bool got = mbar_wait_stage(&tfull_bar[buf], (tb >> 1) & 1u, s_abort, p.status, p.wait_ns);
+        if (!epilogue_all(wg, got)) return false;
+        tc_fence_after();
+        tbase = tmem_base + (uint32_t(q * 32) << 16) + buf * TMEM_BUF;
+        return true;
+      };
+      auto release = [&]() {   // its values are in registers: hand it back
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_rank(&tempty_bar[tb & 1u], 0);
+        ++tb;
+      };
+      uint32_t tbase;
+      if constexpr (!PROMOTE) {
+        if (!accumulator(tbase)) break;
+        for (int c = 0; c < t.nrows; c += 32) {
+          float v[32];
+          tmem_ld32(tbase + uint32_t(c), v);
+          tmem_ld_wait();
+          if (c + 32 >= t.nrows) release();
+          put(c, v);
+        }
+      } else {
+        float acc[4][32];
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[cc][j] = 0.0f;
+        bool ok = true;
+        for (int kb = 0; kb < t.nk; kb += SEGMENT) {
+          if (!accumulator(tbase)) { ok = false; break; }
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            if (wg * 128 + cc * 32 < t.nrows) {
+              float v[32];
+              tmem_ld32(tbase + uint32_t(wg * 128 + cc * 32), v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) acc[cc][j] += v[j];
+            }
+          }
+          release();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc)
+          if (wg * 128 + cc * 32 < t.nrows) put(wg * 128 + cc * 32, acc[cc]);
+      }
     }
-    if (warp == FIRST_EPI_WARP && lane == 0) bulk_wait0();   // stores complete before the CTA exits
-  }
-  // ------------------------------------------------------------------ teardown
-  __syncthreads();
-  if (warp == 0 && lane == 0) {
-    // copies issued but never relayed (only after an abort) must land first
-    int never = 0;
-    for (uint32_t j = s_relayed; j < s_issued; ++j)
-      if (j != s_withheld) mbar_wait_stage(&full_bar[j % STAGES], (j / STAGES) & 1u, &never, p.status, p.wait_ns);
-  }
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();   // both CTAs are past their last remote arrival and MMA
-  if (warp == 1) {
+    if (storer) bulk_wait0();   // stores complete before the CTA exits
+    // ------------------------------------------------ teardown (epilogue side)
     __syncwarp();
-    tc_fence_after();
-    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    asm volatile("bar.sync 0;" ::: "memory");
+    tc_fence_before();
+    asm volatile("bar.sync 0;" ::: "memory");
+    cluster_sync();
+    cluster_sync();
   }
-  cluster_sync();
 }
 
-template <int MODE, int BR>
-cudaError_t launch_mode(const moe_layer_s* L, const CUtensorMap& tmA, const RowMaps& tmB, GmmArgs a, long long tiles,
+template <int MODE, int BR, bool PROMOTE>
+cudaError_t launch_variant(const moe_layer_s* L, const CUtensorMap& tmA, const RowMaps& tmB, GmmArgs a, long long tiles,
                         cudaStream_t st) {
   // bulk stores want the base and the row stride in 16-byte units; 16-bit
   // accumulation rounds once, which a bulk add to the 16-bit values would not
@@ -486,7 +569,15 @@ cudaError_t launch_mode(const moe_layer_s* L, const CUtensorMap& tmA, const RowM
     return cudaErrorInvalidValue;
   static std::atomic<bool> configured[kMaxDevices];   // the attribute is per device
   cudaError_t ce = once_per_device(configured, []() {
-    return cudaFuncSetAttribute(grouped_mm_kernel<MODE, BR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_dyn(BR));
+    // setmaxnreg.inc waits for registers that come only from this CTA's
+    // launch allocation: refuse a build whose count cannot fund the split
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, grouped_mm_kernel<MODE, BR, PROMOTE>);
+    if (e != cudaSuccess) return e;
+    if (PROMOTE && fa.numRegs * threads(PROMOTE) < 128 * PRODUCER_REGS + 256 * EPILOGUE_REGS)
+      return cudaErrorInvalidConfiguration;
+    return cudaFuncSetAttribute(grouped_mm_kernel<MODE, BR, PROMOTE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                smem_dyn(BR, PROMOTE));
   });
   if (ce != cudaSuccess) return ce;
   a.wait_ns = kWaitLimitNs;
@@ -497,7 +588,17 @@ cudaError_t launch_mode(const moe_layer_s* L, const CUtensorMap& tmA, const RowM
   }
   const long long pairs = tiles < L->num_sms / 2 ? tiles : L->num_sms / 2;
   if (pairs <= 0) return cudaSuccess;
-  return launch_pdl(grouped_mm_kernel<MODE, BR>, dim3(unsigned(2 * pairs)), dim3(THREADS), smem_dyn(BR), st, tmA, tmB, tmO, a);
+  return launch_pdl(grouped_mm_kernel<MODE, BR, PROMOTE>, dim3(unsigned(2 * pairs)), dim3(threads(PROMOTE)),
+                    smem_dyn(BR, PROMOTE), st, tmA, tmB, tmO, a);
+}
+
+// `terms`: the longest contraction that the launch may hold.
+template <int MODE, int BR>
+cudaError_t launch_mode(const moe_layer_s* L, const CUtensorMap& tmA, const RowMaps& tmB, const GmmArgs& a, int terms,
+                        long long tiles, cudaStream_t st) {
+  if (a.out_type == MOE_F32 && terms > SEGMENT * BK)
+    return launch_variant<MODE, BR, true>(L, tmA, tmB, a, tiles, st);
+  return launch_variant<MODE, BR, false>(L, tmA, tmB, a, tiles, st);
 }
 
 // A row operand [rows][cols] whose rows are the tile's N (K-major boxes).
@@ -534,7 +635,8 @@ cudaError_t launch_grouped_mm(const moe_layer_s* L, int mode, moe_dtype t, const
     if (!encode_tmap_16(&tmA, t, b, k, rows, 0, ldb, 64, 64) || !encode_tmap_16(&tmB.m[0], t, a, n, rows, 0, lda, 64, 64))
       return cudaErrorInvalidValue;
     for (int j = 1; j < 4; ++j) tmB.m[j] = tmB.m[0];
-    return launch_mode<MOE_MM_WGRAD, 256>(L, tmA, tmB, p, static_cast<long long>(G) * ((n + 255) / 256) * p.ntc, st);
+    return launch_mode<MOE_MM_WGRAD, 256>(L, tmA, tmB, p, rows,
+                                           static_cast<long long>(G) * ((n + 255) / 256) * p.ntc, st);
   }
   // a = the rows, b = w [G][n][k]
   const int contraction = mode == MOE_MM_FORWARD ? k : n;
@@ -549,10 +651,10 @@ cudaError_t launch_grouped_mm(const moe_layer_s* L, int mode, moe_dtype t, const
   // upper bound on the tiles: every group may add one partial row tile
   const long long tiles = (static_cast<long long>(rows) / br + (rows < G ? rows : G)) * p.ntc;
   if (mode == MOE_MM_FORWARD)
-    return br == 64 ? launch_mode<MOE_MM_FORWARD, 64>(L, tmA, tmB, p, tiles, st)
-                    : launch_mode<MOE_MM_FORWARD, 256>(L, tmA, tmB, p, tiles, st);
-  return br == 64 ? launch_mode<MOE_MM_DGRAD, 64>(L, tmA, tmB, p, tiles, st)
-                  : launch_mode<MOE_MM_DGRAD, 256>(L, tmA, tmB, p, tiles, st);
+    return br == 64 ? launch_mode<MOE_MM_FORWARD, 64>(L, tmA, tmB, p, contraction, tiles, st)
+                    : launch_mode<MOE_MM_FORWARD, 256>(L, tmA, tmB, p, contraction, tiles, st);
+  return br == 64 ? launch_mode<MOE_MM_DGRAD, 64>(L, tmA, tmB, p, contraction, tiles, st)
+                  : launch_mode<MOE_MM_DGRAD, 256>(L, tmA, tmB, p, contraction, tiles, st);
 }
 
 }  // namespace moe
