@@ -1,11 +1,14 @@
 """PyTorch plumbing for the library: device copies of a layer's weights,
-workspace allocation and bf16 bit-pattern conversions. No layer arithmetic."""
+workspace allocation, bf16 bit-pattern conversions and the packing of 4-bit
+weights. No layer arithmetic."""
 from __future__ import annotations
 
 import numpy as np
 import torch
 
-from . import LayerWeights, MoeLayer, moe_workspace_size
+from . import MOE_BF16, MOE_F16, MOE_F32, LayerWeights, MoeLayer, W4Weights, moe_workspace_size
+
+TYPE_CODES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}   # moe_dtype
 
 
 def to_device(a: np.ndarray, device="cuda") -> torch.Tensor:
@@ -53,3 +56,36 @@ def workspace(layer: MoeLayer, T: int, device="cuda") -> torch.Tensor:
     if n == 0:
         raise ValueError("moe_workspace_size returned 0")
     return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def w4_quantize(w: torch.Tensor, group: int = 128, zeros: bool = False, scale_dtype=torch.bfloat16) -> W4Weights:
+    """4-bit weights (round to nearest) of w [experts][n][k], for moe_w4_matvec
+    and moe_w4_gate_up: one scale per `group` columns of a row, the largest
+    magnitude at +-7 steps around a fixed zero point of 8, or, with `zeros`,
+    the group's range spread over the 16 codes around its own zero point.
+    An offline step, done once per checkpoint."""
+    G, n, k = w.shape
+    ng, ld = -(-k // group), -(-((k + 1) // 2) // 16) * 16
+    v = torch.nn.functional.pad(w.float(), (0, ng * group - k)).view(G, n, ng, group)
+    if zeros:
+        lo, hi = v.amin(-1).clamp(max=0), v.amax(-1).clamp(min=0)
+        scales = ((hi - lo) / 15).to(scale_dtype)
+    else:
+        scales = (v.abs().amax(-1) / 7).to(scale_dtype)
+    step = scales.float()
+    step = torch.where(step > 0, step, torch.ones_like(step))   # a group of zeros: every code is its zero point
+    z = (-lo / step).round().clamp(0, 15) if zeros else torch.full_like(step, 8.0)
+    q = ((v / step[..., None]).round() + z[..., None]).clamp(0, 15).to(torch.uint8).view(G, n, -1)[:, :, :k]
+    codes = torch.zeros(G, n, 2 * ld, dtype=torch.uint8, device=w.device)
+    codes[:, :, :k] = q
+    codes = codes[:, :, 0::2] | (codes[:, :, 1::2] << 4)
+    return W4Weights(codes.contiguous(), scales.contiguous(), z.to(torch.uint8).contiguous() if zeros else None,
+                     TYPE_CODES[scale_dtype], group)
+
+
+def w4_values(w: W4Weights, k: int) -> torch.Tensor:
+    """The float32 values [experts][n][k] that 4-bit weights stand for."""
+    G, n, _ = w.codes.shape
+    q = torch.stack((w.codes & 15, w.codes >> 4), -1).view(G, n, -1)[:, :, :k].float()
+    wide = lambda t: t.float().repeat_interleave(w.desc.group, -1)[:, :, :k]  # noqa: E731
+    return (q - (8.0 if w.zeros is None else wide(w.zeros))) * wide(w.scales)
