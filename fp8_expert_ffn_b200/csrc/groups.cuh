@@ -47,17 +47,26 @@ struct GroupPlan {
 template <int THREADS, typename F>
 __device__ __forceinline__ int build_plan(GroupPlan& s, const int32_t* __restrict__ offsets, int ngroups, int nweights,
                                           int rows, uint32_t* status, F count) {
+  constexpr int ROUNDS = (kMaxGroups + THREADS - 1) / THREADS;
+  int o0[ROUNDS], o1[ROUNDS];   // all loads first: one trip to memory
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) {
+    const int g = r * THREADS + int(threadIdx.x);
+    o0[r] = g < ngroups ? offsets[g] : 0;
+    o1[r] = g < ngroups ? offsets[g + 1] : 0;
+  }
   int base = 0;
   int bad_any = 0;
-  for (int g0 = 0; g0 < ngroups; g0 += THREADS) {
-    const int g = g0 + int(threadIdx.x);
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) {
+    if (r * THREADS >= ngroups) break;
+    const int g = r * THREADS + int(threadIdx.x);
     int v = 0, bad = 0;
     if (g < ngroups) {
-      const int o0 = offsets[g], o1 = offsets[g + 1];
-      bad = o0 < 0 || o1 < o0 || o1 > rows || (g >= nweights && o1 != o0);
-      s.off[g] = o0;
-      if (g == ngroups - 1) s.off[ngroups] = o1;
-      if (!bad && g < nweights) v = count(o1 - o0);
+      bad = o0[r] < 0 || o1[r] < o0[r] || o1[r] > rows || (g >= nweights && o1[r] != o0[r]);
+      s.off[g] = o0[r];
+      if (g == ngroups - 1) s.off[ngroups] = o1[r];
+      if (!bad && g < nweights) v = count(o1[r] - o0[r]);
     }
     int incl = v;
 #pragma unroll

@@ -116,15 +116,13 @@ __device__ __forceinline__ uint4 ldg128(const void* a) {
   asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a));
   return v;
 }
-__device__ __forceinline__ uint4 ldg128_or_zero(const void* a, bool there) {
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+__device__ __forceinline__ void ldg128_if(uint4& v, const void* a, bool there) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %5, 0;\n\t"
       "@p ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
       : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
       : "l"(a), "r"(int(there)));
-  return v;
 }
 __device__ __forceinline__ uint2 ldg64(const void* a) {
   uint2 v;
@@ -277,14 +275,14 @@ __device__ __forceinline__ void unpack_scales(const W4Args& p, const Scales<GPS>
 }
 
 // A lane's 8-column pieces of NT x 8 rows of x in NC 32-column chunks from
-// column `at` on.
+// column `at` on. Rows that are not there keep what x holds (zeros).
 template <typename T, int NT, int NC>
 __device__ __forceinline__ void load_x(const T* const (&xrow)[NT], bool edge, int at, int k, uint4 (&x)[NT][NC]) {
   if (!edge) {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int c = 0; c < NC; ++c) x[j][c] = ldg128_or_zero(xrow[j] + at + c * 32, xrow[j] != nullptr);
+      for (int c = 0; c < NC; ++c) ldg128_if(x[j][c], xrow[j] + at + c * 32, xrow[j] != nullptr);
   } else {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -475,6 +473,12 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.0f;
     // x runs one half ahead of its use, the scales one stage
     uint4 x[2][NT][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[i][j][c] = make_uint4(0u, 0u, 0u, 0u);
     Scales<KB / GS> sc, sn;
     const int hend = min(2 * kb1, (p.k + KH - 1) / KH);   // halves past the row's end hold nothing
     auto ahead = [&](int hk, uint4 (&xx)[NT][4]) {
@@ -620,8 +624,9 @@ cudaError_t launch_w4(const moe_layer_s* L, moe_dtype t, const void* x, int x_ro
   // only way to fill the machine with few experts), fewer leave more blocks
   // per unit to pay for its fixed cost (finding it, joining the partial sums:
   // about one block's time). The split with the shortest longest CTA:
-  // units per column tile, at most
-  const long long groups = rows / (8 * nt) + (rows < G ? rows : G);
+  // units per column tile, at most: a group adds at most one that is not full
+  long long groups = rows / (8 * nt) + (rows < G ? rows : G);
+  if (groups > rows) groups = rows;
   const long long ctas = static_cast<long long>(CTAS_PER_SM) * L->num_sms;
   long long best = 0;
   for (int wk = WARPS; wk >= 1; wk /= 2) {
