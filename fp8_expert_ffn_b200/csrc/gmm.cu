@@ -114,35 +114,77 @@ struct Tile {
   // weight for wgrad); nrows: valid rows; r_first, wgrad: the group's first row
 };
 
-template <int MODE, int BR>
-__device__ __forceinline__ Tile decode_tile(int i, const GroupPlan& s, const GmmArgs& p) {
-  Tile t;
-  t.g = find_group(s.prefix, p.ngroups, i);
-  const int local = i - s.prefix[t.g];
-  const int g0 = s.off[t.g], n_g = s.off[t.g + 1] - g0;
-  if (MODE == MOE_MM_WGRAD) {
-    const int rt = local / p.ntc;
-    t.col0 = (local - rt * p.ntc) * BC;
-    t.row0 = rt * BR;
-    t.nrows = min(BR, p.nr - t.row0);
-    t.r_first = g0;
-    t.nk = (n_g + BK - 1) / BK;
-  } else {
-    // chunks of up to 8 row tiles, then the column tiles, then the row tiles:
-    // the row tiles that share a weight tile run side by side
-    const int rts = (n_g + BR - 1) / BR;
-    const int per_chunk = RCHUNK * p.ntc;
-    const int chunk = local / per_chunk;
-    const int within = local - chunk * per_chunk;
-    const int rc = min(RCHUNK, rts - chunk * RCHUNK);
-    const int ct = within / rc;
-    const int rt = chunk * RCHUNK + (within - ct * rc);
-    t.col0 = ct * BC;
-    t.row0 = g0 + rt * BR;
-    t.nrows = min(BR, n_g - rt * BR);
-    t.r_first = 0;
-    t.nk = p.nk;
+// The tile list. Forward and dgrad keep the groups' order: a group's weights
+// and rows are in use by all pairs at one time and come from HBM once. (Full
+// tiles first and the groups' partial ones behind them, largest first, would
+// end the busiest pair 1.5% behind the mean instead of 10%, and still took
+// 417 us instead of 396 on the training batch: the tensor cores run at the
+// power limit, where a second reading of the weights costs more than idle
+// pairs.) wgrad takes the groups by falling rows, so that the tiles of one
+// round cost the same (FFN 1500 case 408 -> 394 us).
+struct TileList {
+  GroupPlan plan;                 // prefix: of the tiles (not for wgrad)
+  int key[kMaxGroups];            // wgrad: rows of the groups
+  uint16_t order[kMaxGroups];     // and the groups by falling rows
+  int total;
+};
+
+template <int MODE, int BR, int THREADS>
+__device__ __forceinline__ void build_tiles(TileList& s, const GmmArgs& p) {
+  int n = build_plan<THREADS>(s.plan, p.offsets, p.ngroups, p.nweights, p.rows, p.status, [&](int n_g) -> int {
+    return MODE == MOE_MM_WGRAD ? 0 : (n_g + BR - 1) / BR * p.ntc;
+  });
+  if (MODE == MOE_MM_WGRAD && n >= 0) {
+    n = p.nweights * ((p.nr + BR - 1) / BR) * p.ntc;   // groups without rows too
+    for (int g = threadIdx.x; g < p.nweights; g += THREADS) s.key[g] = s.plan.off[g + 1] - s.plan.off[g];
+    __syncthreads();
+    for (int g = threadIdx.x; g < p.nweights; g += THREADS) {
+      const int key = s.key[g];
+      int rank = 0;
+      for (int j = 0; j < p.nweights; ++j) rank += s.key[j] > key || (s.key[j] == key && j < g);
+      s.order[rank] = uint16_t(g);
+    }
   }
+  if (threadIdx.x == 0) s.total = n < 0 ? 0 : n;
+}
+
+// The tile that pair `pair` of `npairs` takes in round w (the direction
+// alternates, so that the first pairs do not get the larger of every round).
+__device__ __forceinline__ int tile_at(int w, int pair, int npairs) {
+  return w * npairs + ((w & 1) ? npairs - 1 - pair : pair);
+}
+
+template <int MODE, int BR>
+__device__ __forceinline__ Tile decode_tile(int i, const TileList& s, const GmmArgs& p) {
+  Tile t;
+  if (MODE == MOE_MM_WGRAD) {
+    const int ct = i / p.ntc;                       // (group, row tile)
+    const int rts = (p.nr + BR - 1) / BR;
+    t.g = s.order[ct / rts];
+    t.col0 = (i - ct * p.ntc) * BC;
+    t.row0 = (ct % rts) * BR;
+    t.nrows = min(BR, p.nr - t.row0);
+    t.r_first = s.plan.off[t.g];
+    t.nk = (s.plan.off[t.g + 1] - t.r_first + BK - 1) / BK;
+    return t;
+  }
+  t.r_first = 0;
+  t.nk = p.nk;
+  // chunks of up to 8 row tiles, then the column tiles, then the row tiles:
+  // the row tiles that share a weight tile run side by side
+  t.g = find_group(s.plan.prefix, p.ngroups, i);
+  const int local = i - s.plan.prefix[t.g];
+  const int g0 = s.plan.off[t.g], n_g = s.plan.off[t.g + 1] - g0;
+  const int rts = (n_g + BR - 1) / BR;
+  const int per_chunk = RCHUNK * p.ntc;
+  const int chunk = local / per_chunk;
+  const int within = local - chunk * per_chunk;
+  const int rc = min(RCHUNK, rts - chunk * RCHUNK);
+  const int ct = within / rc;
+  const int rt = chunk * RCHUNK + (within - ct * rc);
+  t.col0 = ct * BC;
+  t.row0 = g0 + rt * BR;
+  t.nrows = min(BR, n_g - rt * BR);
   return t;
 }
 
@@ -218,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
   __shared__ __align__(8) uint64_t tfull_bar[2];
   __shared__ __align__(8) uint64_t tempty_bar[2];       // leading CTA: both CTAs' epilogues
   __shared__ __align__(8) uint64_t done_bar;
-  __shared__ GroupPlan s_plan;
+  __shared__ TileList s_tiles;
   __shared__ uint32_t tmem_base_s;
   __shared__ int s_abort_store;
   __shared__ uint32_t s_relayed, s_issued, s_withheld;
@@ -257,16 +299,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  const int total = build_plan<THREADS>(
-      s_plan, p.offsets, p.ngroups, p.nweights, p.rows, p.status, [&](int n_g) -> int {
-        if (MODE == MOE_MM_WGRAD) return ((p.nr + BR - 1) / BR) * p.ntc;
-        return ((n_g + BR - 1) / BR) * p.ntc;
-      });
+  build_tiles<MODE, BR, THREADS>(s_tiles, p);
   tc_fence_before();
   __syncthreads();
   cluster_sync();   // the peer's barriers are initialised and its TMEM is allocated
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_s;
+  const int total = s_tiles.total;
 
   if (warp < FIRST_EPI_WARP) {
   if (PROMOTE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PRODUCER_REGS));
@@ -275,8 +314,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
     if (elect_one()) {
       uint32_t it = 0;
       bool ok = true;
-      for (int i = pair; ok && i < total; i += npairs) {
-        const Tile t = decode_tile<MODE, BR>(i, s_plan, p);
+      for (int w = 0, i; ok && (i = tile_at(w, pair, npairs)) < total; ++w) {
+        const Tile t = decode_tile<MODE, BR>(i, s_tiles, p);
         const int half = tile_n(t) >> 1;
         const int acol = t.col0 + int(rank) * 128;
         const int brow = t.row0 + int(rank) * half;
@@ -324,8 +363,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
     if (rank == 0 && elect_one()) {
       uint32_t it = 0, tb = 0;
       bool ok = true;
-      for (int i = pair; ok && i < total; i += npairs) {
-        const Tile t = decode_tile<MODE, BR>(i, s_plan, p);
+      for (int w = 0, i; ok && (i = tile_at(w, pair, npairs)) < total; ++w) {
+        const Tile t = decode_tile<MODE, BR>(i, s_tiles, p);
         if (t.nk == 0) continue;
         const uint32_t idesc = p.idesc | (uint32_t(tile_n(t) >> 3) << 17);
         for (int kb = 0; kb < t.nk; ++kb) {
@@ -366,10 +405,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
     // ----------------------------------------------------------------- relay
     uint32_t it = 0;
     bool ok = true;
-    for (int i = pair; ok && i < total; i += npairs) {
-      const Tile t = decode_tile<MODE, BR>(i, s_plan, p);
+    for (int w = 0, i; ok && (i = tile_at(w, pair, npairs)) < total; ++w) {
+      const Tile t = decode_tile<MODE, BR>(i, s_tiles, p);
       int left = 0;   // wgrad: the group's rows from the current block on
-      if (MODE == MOE_MM_WGRAD) left = s_plan.off[t.g + 1] - t.r_first;
+      if (MODE == MOE_MM_WGRAD) left = s_tiles.plan.off[t.g + 1] - t.r_first;
       for (int kb = 0; kb < t.nk; ++kb) {
         const int s = it % STAGES;
         const bool got = mbar_wait_stage(&full_bar[s], (it / STAGES) & 1u, s_abort, p.status, p.wait_ns);
@@ -424,8 +463,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
     const bool storer = q == 0 && lane == 0;          // one thread per warpgroup issues the bulk stores
     uint8_t* staging = smem + STAGES * STAGE_BYTES + wg * 2 * STG_BYTES;
     uint32_t tb = 0, sb = 0;
-    for (int i = pair; i < total; i += npairs) {
-      const Tile t = decode_tile<MODE, BR>(i, s_plan, p);
+    for (int w = 0, i; (i = tile_at(w, pair, npairs)) < total; ++w) {
+      const Tile t = decode_tile<MODE, BR>(i, s_tiles, p);
       const int x = t.col0 + int(rank) * 128;
       const int col = x + q * 32 + lane;
       const bool cv = col < p.nc;
@@ -494,7 +533,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
       // of the warpgroup together, since they share barriers)
       auto accumulator = [&](uint32_t& tbase) {
         const uint32_t buf = tb & 1u;
-        const bool got = mbar_wait_stage(&tfull_bar[buf], (tb >> 1) & 1u, s_abort, p.status, p.wait_ns);
+        // one warp polls, the others sleep in the barrier
+        const bool got =
+            q != 0 || mbar_wait_stage(&tfull_bar[buf], (tb >> 1) & 1u, s_abort, p.status, p.wait_ns);
         if (!epilogue_all(wg, got)) return false;
         tc_fence_after();
         tbase = tmem_base + (uint32_t(q * 32) << 16) + buf * TMEM_BUF;
