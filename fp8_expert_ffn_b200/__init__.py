@@ -146,10 +146,26 @@ def _ptr(t) -> int:
     return t.data_ptr()
 
 
+_current = None   # () -> the current stream's handle, set up on first use
+
+
+def _current_stream():
+    """The handle of torch's current stream. torch.cuda.current_stream() builds
+    a Stream object for it (3.4 us a call, a third of a small call's time); the
+    raw handle takes 0.3 us where this build of torch offers it."""
+    global _current
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        _current = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    else:
+        _current = lambda: raw(torch.cuda.current_device())  # noqa: E731
+    return _current()
+
+
 def _stream(stream) -> int:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream() if _current is None else _current()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -656,3 +656,25 @@ def test_timed_out_wait_is_reported_and_the_handle_recovers(name):
     status_ok(gr.layer)
     for got, want in zip(out, base):
         assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+def test_calls_go_to_the_current_stream():
+    """Without a stream argument a call is ordered on torch's current stream,
+    whichever that is."""
+    rng = np.random.default_rng(11)
+    L = make_layer(1, 0)
+    rows, f = 4096, 2048
+    u = normal(rng, (rows, f)).to(F32)
+    side = torch.cuda.Stream()
+    for stream in (torch.cuda.current_stream(), side, torch.cuda.default_stream()):
+        assert fx._stream(None) == torch.cuda.current_stream().cuda_stream
+        with torch.cuda.stream(stream):
+            assert fx._stream(None) == stream.cuda_stream
+            g = torch.zeros(rows, f, device="cuda")
+            for _ in range(20):
+                g.add_(0.1)                      # still running when the call is made
+            h = torch.empty_like(g)
+            fx.moe_swiglu(L, fx.MOE_F32, g, f, u, f, None, rows, f, h, f)
+        stream.synchronize()
+        want = swiglu_reference(g, u)
+        assert torch.allclose(h.double(), want, rtol=1e-5, atol=1e-6)
