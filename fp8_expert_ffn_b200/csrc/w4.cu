@@ -27,6 +27,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cmath>
 #include <type_traits>
 
 #include "common.cuh"
@@ -400,7 +401,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   const int total = build_plan<THREADS>(s_plan, p.offsets, p.ngroups, p.nweights, p.rows, p.status,
                                         [&](int n_g) -> int { return ((n_g + RMAX - 1) / RMAX) * p.ntn; });
 
-  const int kb0 = kw * p.nkb / p.wk, kb1 = (kw + 1) * p.nkb / p.wk;   // this warp's blocks of a tile
+  // This warp's stages of a unit: every wk-th, so that the warps along the
+  // contraction read neighbouring pieces of the same rows at one time.
+  const int kb0 = kw, kb1 = p.nkb;
   // The ring runs STAGES blocks ahead of use, across tiles; every lane keeps
   // its state and one of them issues the copies.
   const uint32_t ring = smem_u32(smem) + warp * (STAGES * STAGE_BYTES);
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     }
   };
   auto issue = [&]() {   // the next block, if there is one
-    if (i_unit >= total || kb0 == kb1) return;
+    if (i_unit >= total || kb0 >= kb1) return;
     const uint32_t s = issued % STAGES;
     if (issued == withheld) {
       // test only: this block never arrives
@@ -428,7 +431,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       if (p.dual) tma_load_3d(dst + STAGE_BYTES / 2, &tm1, &bar[s], i_kb * (KB / 2), i_row, i_g);
     }
     ++issued;
-    if (++i_kb == kb1) {
+    if ((i_kb += p.wk) >= kb1) {
       i_kb = kb0;
       i_unit += gridDim.x;
       place();
@@ -488,17 +491,17 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       ahead(2 * kb0, x[0]);
       load_scales<ZEROS>(p, sp, zp, srow, kb0, sn);
     }
-    for (int kb = kb0; kb < kb1; ++kb) {
+    for (int kb = kb0; kb < kb1; kb += p.wk) {
       ahead(2 * kb + 1, x[1]);
       sc = sn;
-      if (kb + 1 < kb1) load_scales<ZEROS>(p, sp, zp, srow, kb + 1, sn);
+      if (kb + p.wk < kb1) load_scales<ZEROS>(p, sp, zp, srow, kb + p.wk, sn);
       if (ok) {
         const bool got = mbar_wait_stage(&bar[used % STAGES], (used / STAGES) & 1u, s_abort, p.status, p.wait_ns);
         ok = __all_sync(0xFFFFFFFFu, got);
       }
       const uint32_t st = ring + (used % STAGES) * STAGE_BYTES;
       if (ok) half_mma<BF16, GS, ZEROS, NT, 0>(p, st, acc, sc, x[0], lane);
-      if (kb + 1 < kb1) ahead(2 * kb + 2, x[0]);
+      if (kb + p.wk < kb1) ahead(2 * (kb + p.wk), x[0]);
       if (ok) {
         if (2 * kb + 1 < hend) half_mma<BF16, GS, ZEROS, NT, 1>(p, st, acc, sc, x[1], lane);
         ++used;
@@ -620,20 +623,24 @@ cudaError_t launch_w4(const moe_layer_s* L, moe_dtype t, const void* x, int x_ro
   // Rows of a unit: 8, or 16 when groups hold more than 8 on average (the
   // codes are then unpacked half as often, on two thirds of the warps).
   const int nt = rows > 8ll * G ? 2 : 1;
-  // Warps along the contraction. More of them give more, smaller units (the
-  // only way to fill the machine with few experts), fewer leave more blocks
-  // per unit to pay for its fixed cost (finding it, joining the partial sums:
-  // about one block's time). The split with the shortest longest CTA:
   // units per column tile, at most: a group adds at most one that is not full
   long long groups = rows / (8 * nt) + (rows < G ? rows : G);
   if (groups > rows) groups = rows;
-  const long long ctas = static_cast<long long>(CTAS_PER_SM) * L->num_sms;
-  long long best = 0;
+  // Warps along the contraction. More of them give more, smaller units (the
+  // only way to fill the machine with few experts), fewer leave more stages
+  // per unit to pay for its fixed cost (finding it, joining the partial sums:
+  // half a stage's time). The split with the least expected time of a CTA,
+  // from the groups that evenly spread rows would touch: 4 ways for one token
+  // or one matrix (30.7 us against 34.8 two ways and 53 one way), 2 ways for
+  // a decode batch of 64 (422 against 430 one way and 463 four ways).
+  const double ctas = double(CTAS_PER_SM) * L->num_sms;
+  const double touched = G * (1.0 - exp(-double(rows) / G)) + double(rows) / (16 * nt);
+  double best = 0.0;
   for (int wk = WARPS; wk >= 1; wk /= 2) {
     const int cols = (WARPS / wk) * (p.dual ? BOX_ROWS / 2 : BOX_ROWS);
-    const long long units = groups * ((n + cols - 1) / cols);
-    const long long cost = ((units + ctas - 1) / ctas) * (2 * ((p.nkb + wk - 1) / wk) + 1);
-    if (best == 0 || cost < best) {
+    const double rounds = (touched < double(groups) ? touched : double(groups)) * ((n + cols - 1) / cols) / ctas + 0.5;
+    const double cost = (rounds > 1.0 ? rounds : 1.0) * (2 * ((p.nkb + wk - 1) / wk) + 1);
+    if (best == 0.0 || cost < best) {
       best = cost;
       p.wk = wk;
     }
