@@ -26,10 +26,10 @@
 // independent 128 x 256 tiles would move 48 KB.
 //   warp 0      TMA producer into a ring of 6 stages (16 KB of A, up to 16 KB of B)
 //   warp 1      TMEM allocation; in the leading CTA the MMA issuer
-//   warp 2      relay: waits for its CTA's copies, zeroes a wgrad tail, and
+//   warp 2      relay: waits for its CTA's copies, clears a wgrad tail, and
 //               signals the leading CTA
 //   warp 3      idle
-//   warps 4-    epilogue (4 warps, 8 where it adds parts of a sum): TMEM lanes 32*(w%4).., one output column per lane;
+//   warps 4-11  epilogue, two warpgroups with 128 output rows each: TMEM lanes 32*(w%4).., one output column per lane;
 //               two 256-column TMEM buffers overlap it with the next tile
 // No TMA multicast; commits signal both CTAs. Every wait is bounded (1 s): on
 // a timeout the status word is set, all roles leave, copies in flight are
@@ -71,11 +71,17 @@ constexpr int stage_bytes(int BR) { return A_BYTES + BR * BK; }   // each CTA ho
 // the other warps as in the FP8 GEMMs. 16-bit outputs, whose rounding is a
 // thousand times larger, keep one sum.
 constexpr int SEGMENT = 8;
-constexpr int epi_warps(bool promote) { return promote ? 8 : 4; }
-constexpr int threads(bool promote) { return 32 * (FIRST_EPI_WARP + epi_warps(promote)); }
-constexpr int stages(int BR, bool promote) { return (BR == 64 ? 10 : 6) - (promote ? 1 : 0); }
-constexpr int smem_dyn(int BR, bool promote) {
-  return stages(BR, promote) * stage_bytes(BR) + epi_warps(promote) / 2 * STG_BYTES + 1024;
+
+// Epilogue warps: two warpgroups with 128 rows each, or one where tiles have
+// 64 rows (with one for 256 rows, a weight gradient over 512 rows per group
+// waited for its stores: 11.7 thousand cycles per tile, 4.1 of them MMA).
+constexpr int epi_warps(int BR, bool promote) { return BR == 256 || promote ? 8 : 4; }
+constexpr int threads(int BR, bool promote) { return 32 * (FIRST_EPI_WARP + epi_warps(BR, promote)); }
+constexpr int stages(int BR, bool promote) { return BR == 256 ? 6 : 10; }
+// Two staged chunks: one per warpgroup, or two of the only one; wgrad's zeros
+// (one box) lie behind them.
+constexpr int smem_dyn(int mode, int BR, bool promote) {
+  return stages(BR, promote) * stage_bytes(BR) + 2 * STG_BYTES + (mode == MOE_MM_WGRAD ? BOX_BYTES : 0) + 1024;
 }
 constexpr int LAUNCH_REGS = 168;     // 384 threads, one CTA per SM
 constexpr int PRODUCER_REGS = 40;
@@ -165,7 +171,8 @@ __device__ __forceinline__ Tile decode_tile(int i, const TileList& s, const GmmA
     t.row0 = (ct % rts) * BR;
     t.nrows = min(BR, p.nr - t.row0);
     t.r_first = s.plan.off[t.g];
-    t.nk = (s.plan.off[t.g + 1] - t.r_first + BK - 1) / BK;
+    const int n_g = s.plan.off[t.g + 1] - t.r_first;
+    t.nk = (n_g + BK - 1) / BK;
     return t;
   }
   t.r_first = 0;
@@ -246,13 +253,13 @@ __device__ __forceinline__ bool epilogue_all(int wg, bool ok) {
 }
 
 template <int MODE, int BR, bool PROMOTE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE), 1)
     grouped_mm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ RowMaps tmB,
                       const __grid_constant__ CUtensorMap tmO, const GmmArgs p) {
   constexpr bool A_MN = MODE != MOE_MM_FORWARD;   // A's contraction is its slow dimension
   constexpr bool B_MN = MODE == MOE_MM_WGRAD;
   constexpr int STAGES = stages(BR, PROMOTE), STAGE_BYTES = stage_bytes(BR);
-  constexpr int THREADS = threads(PROMOTE), EPI_WARPS = epi_warps(PROMOTE);
+  constexpr int THREADS = threads(BR, PROMOTE), EPI_WARPS = epi_warps(BR, PROMOTE);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[STAGES];    // this CTA's copies of a stage
   __shared__ __align__(8) uint64_t ready_bar[STAGES];   // leading CTA: both CTAs' stages complete
@@ -260,6 +267,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
   __shared__ __align__(8) uint64_t tfull_bar[2];
   __shared__ __align__(8) uint64_t tempty_bar[2];       // leading CTA: both CTAs' epilogues
   __shared__ __align__(8) uint64_t done_bar;
+  __shared__ __align__(8) uint64_t zero_bar;            // wgrad: zeros copied over a tail
   __shared__ TileList s_tiles;
   __shared__ uint32_t tmem_base_s;
   __shared__ int s_abort_store;
@@ -282,6 +290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
       mbar_init(&tempty_bar[b], 2 * EPI_WARPS);
     }
     mbar_init(&done_bar, 1);
+    mbar_init(&zero_bar, 1);
     s_abort_store = 0;
     s_relayed = 0;
     s_issued = 0;
@@ -378,7 +387,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
           const uint32_t d = tmem_base + buf * TMEM_BUF;
           const int s = it % STAGES;
           if (!mbar_wait_stage(&ready_bar[s], (it / STAGES) & 1u, s_abort, p.status, p.wait_ns)) { ok = false; break; }
-          if (MODE == MOE_MM_WGRAD && kb == t.nk - 1) cluster_fence();   // the relays' zeros
           tc_fence_after();
           const uint32_t a_addr = smem_u32(smem + s * STAGE_BYTES);
           const uint64_t ad = A_MN ? smem_desc_mn_sw128(a_addr, BOX_BYTES) : smem_desc_sw128(a_addr);
@@ -403,6 +411,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
     }
   } else if (warp == 2) {
     // ----------------------------------------------------------------- relay
+    uint8_t* zeros = smem + STAGES * STAGE_BYTES + 2 * STG_BYTES;
+    uint32_t zero_phase = 0;
+    if (MODE == MOE_MM_WGRAD) {
+      for (int v = lane; v < BOX_BYTES / 16; v += 32) reinterpret_cast<uint4*>(zeros)[v] = make_uint4(0u, 0u, 0u, 0u);
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
     uint32_t it = 0;
     bool ok = true;
     for (int w = 0, i; ok && (i = tile_at(w, pair, npairs)) < total; ++w) {
@@ -416,15 +431,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
         if (MODE == MOE_MM_WGRAD) {
           if (left < BK) {
             // rows [left, 64) of every box belong to the next group (or lie
-            // past the last row): set them to zero
-            const int boxes = 2 + ((tile_n(t) / 2 + 63) >> 6);
-            uint8_t* first = smem + s * STAGE_BYTES + lane * 16;   // four 128-byte rows per warp store
-            for (int bx = 0; bx < boxes; ++bx)
-              for (int r = left * 128; r < BOX_BYTES - lane * 16; r += 512)
-                *reinterpret_cast<uint4*>(first + bx * BOX_BYTES + r) = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
+            // past the last row): zeros are copied over them
+            if (elect_one()) {
+              const int boxes = 2 + ((tile_n(t) / 2 + 63) >> 6);
+              const uint32_t bytes = uint32_t(BK - left) * 128u;
+              mbar_arrive_expect_tx(&zero_bar, boxes * bytes);
+              for (int bx = 0; bx < boxes; ++bx)
+                bulk_copy_smem(smem + s * STAGE_BYTES + bx * BOX_BYTES + left * 128, zeros, bytes, &zero_bar);
+            }
             __syncwarp();
-            cluster_fence();   // the leading CTA's MMAs read these zeros
+            const bool clean = mbar_wait_stage(&zero_bar, zero_phase, s_abort, p.status, p.wait_ns);
+            zero_phase ^= 1u;
+            if (!__all_sync(0xFFFFFFFFu, clean)) {
+              // the copies must land before the CTA ends
+              int never = 0;
+              mbar_wait_stage(&zero_bar, zero_phase ^ 1u, &never, p.status, p.wait_ns);
+              ok = false;
+              break;
+            }
           }
           left -= BK;
         }
@@ -459,9 +483,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
     // every instruction that they meet)
     if (PROMOTE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPILOGUE_REGS));
     const int q = warp & 3;                           // TMEM lane quarter this warp may access
-    const int wg = (warp - FIRST_EPI_WARP) >> 2;      // PROMOTE: the half of the rows
-    const bool storer = q == 0 && lane == 0;          // one thread per warpgroup issues the bulk stores
-    uint8_t* staging = smem + STAGES * STAGE_BYTES + wg * 2 * STG_BYTES;
+    const int wg = (warp - FIRST_EPI_WARP) >> 2;      // rows [128 wg, 128 wg + 128) of a tile
+    constexpr int STG_BUFS = EPI_WARPS == 8 ? 1 : 2;  // staging buffers of a warpgroup
+    uint8_t* staging = smem + STAGES * STAGE_BYTES + wg * STG_BYTES;
     uint32_t tb = 0, sb = 0;
     for (int w = 0, i; (i = tile_at(w, pair, npairs)) < total; ++w) {
       const Tile t = decode_tile<MODE, BR>(i, s_tiles, p);
@@ -481,10 +505,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (h == parts) break;
-            // the last store but one has read the buffer that is written now
-            if (storer) bulk_wait_read1();
+            // the last store from the buffer that is written now has read it
+            // (elect_one: always the same thread issues and waits)
+            if (q == 0 && elect_one()) {
+              if (STG_BUFS == 1)
+                bulk_wait_read0();
+              else
+                bulk_wait_read1();
+            }
             epilogue_sync(wg);
-            uint8_t* stg = staging + (sb & 1u) * STG_BYTES;
+            uint8_t* stg = staging + (sb % STG_BUFS) * STG_BYTES;
             if (p.out_type == MOE_F32) {
               float* o = reinterpret_cast<float*>(stg) + q * 32 + lane;
 #pragma unroll
@@ -500,7 +530,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
             }
             fence_proxy_async_smem();
             epilogue_sync(wg);
-            if (storer) {
+            if (q == 0 && elect_one()) {
               const int y = t.row0 + c + 16 * h;
               if (MODE == MOE_MM_WGRAD) {
                 if (x < p.nc && y < p.nr) {
@@ -520,12 +550,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
           store_chunk(p, at + size_t(c) * size_t(p.ld), v, m);
         }
       };
+      const int c0 = wg * 128, c1 = min(t.nrows, c0 + 128);   // this warpgroup's rows
       if (t.nk == 0) {   // wgrad of a group without rows
-        if (!p.accumulate && wg == 0) {
+        if (!p.accumulate) {
           float z[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) z[j] = 0.0f;
-          for (int c = 0; c < t.nrows; c += 32) put(c, z);
+          for (int c = c0; c < c1; c += 32) put(c, z);
         }
         continue;
       }
@@ -550,11 +581,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
       uint32_t tbase;
       if constexpr (!PROMOTE) {
         if (!accumulator(tbase)) break;
-        for (int c = 0; c < t.nrows; c += 32) {
+        if (c0 >= c1) release();
+        for (int c = c0; c < c1; c += 32) {
           float v[32];
           tmem_ld32(tbase + uint32_t(c), v);
           tmem_ld_wait();
-          if (c + 32 >= t.nrows) release();
+          if (c + 32 >= c1) release();
           put(c, v);
         }
       } else {
@@ -568,9 +600,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
           if (!accumulator(tbase)) { ok = false; break; }
 #pragma unroll
           for (int cc = 0; cc < 4; ++cc) {
-            if (wg * 128 + cc * 32 < t.nrows) {
+            if (c0 + cc * 32 < c1) {
               float v[32];
-              tmem_ld32(tbase + uint32_t(wg * 128 + cc * 32), v);
+              tmem_ld32(tbase + uint32_t(c0 + cc * 32), v);
               tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 32; ++j) acc[cc][j] += v[j];
@@ -581,10 +613,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(PROMOTE), 1)
         if (!ok) break;
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc)
-          if (wg * 128 + cc * 32 < t.nrows) put(wg * 128 + cc * 32, acc[cc]);
+          if (c0 + cc * 32 < c1) put(c0 + cc * 32, acc[cc]);
       }
     }
-    if (storer) bulk_wait0();   // stores complete before the CTA exits
+    if (q == 0 && elect_one()) bulk_wait0();   // stores complete before the CTA exits
     // ------------------------------------------------ teardown (epilogue side)
     __syncwarp();
     asm volatile("bar.sync 0;" ::: "memory");
@@ -615,10 +647,10 @@ cudaError_t launch_variant(const moe_layer_s* L, const CUtensorMap& tmA, const R
     cudaFuncAttributes fa;
     cudaError_t e = cudaFuncGetAttributes(&fa, grouped_mm_kernel<MODE, BR, PROMOTE>);
     if (e != cudaSuccess) return e;
-    if (PROMOTE && fa.numRegs * threads(PROMOTE) < 128 * PRODUCER_REGS + 256 * EPILOGUE_REGS)
+    if (PROMOTE && fa.numRegs * threads(BR, PROMOTE) < 128 * PRODUCER_REGS + 256 * EPILOGUE_REGS)
       return cudaErrorInvalidConfiguration;
     return cudaFuncSetAttribute(grouped_mm_kernel<MODE, BR, PROMOTE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                smem_dyn(BR, PROMOTE));
+                                smem_dyn(MODE, BR, PROMOTE));
   });
   if (ce != cudaSuccess) return ce;
   a.wait_ns = kWaitLimitNs;
@@ -629,8 +661,8 @@ cudaError_t launch_variant(const moe_layer_s* L, const CUtensorMap& tmA, const R
   }
   const long long pairs = tiles < L->num_sms / 2 ? tiles : L->num_sms / 2;
   if (pairs <= 0) return cudaSuccess;
-  return launch_pdl(grouped_mm_kernel<MODE, BR, PROMOTE>, dim3(unsigned(2 * pairs)), dim3(threads(PROMOTE)),
-                    smem_dyn(BR, PROMOTE), st, tmA, tmB, tmO, a);
+  return launch_pdl(grouped_mm_kernel<MODE, BR, PROMOTE>, dim3(unsigned(2 * pairs)), dim3(threads(BR, PROMOTE)),
+                    smem_dyn(MODE, BR, PROMOTE), st, tmA, tmB, tmO, a);
 }
 
 // `terms`: the longest contraction that the launch may hold.

@@ -34,11 +34,10 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // Arrives once on the barrier at the same address in CTA `rank` of the
-// cluster. The arrival orders what hardware units wrote (copies and MMAs that
-// this thread has waited for); a thread's own stores to shared memory that
-// the other CTA's MMAs are to see need cluster_fence on both sides. (With
-// .release.cluster and .acquire.cluster on every stage instead, the two
-// fences cost a microsecond per stage.)
+// cluster. The arrival orders what hardware units wrote or read (copies and
+// MMAs that this thread has waited for); a thread's own stores to shared
+// memory for the other CTA would need cluster-scope release and acquire,
+// which cost half a microsecond each.
 __device__ __forceinline__ void mbar_arrive_rank(uint64_t* bar, uint32_t rank) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\t"
@@ -48,7 +47,13 @@ __device__ __forceinline__ void mbar_arrive_rank(uint64_t* bar, uint32_t rank) {
       : "memory");
 }
 
-__device__ __forceinline__ void cluster_fence() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// Bulk copy within this CTA's shared memory (16-byte units), arriving on `bar`.
+__device__ __forceinline__ void bulk_copy_smem(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "r"(smem_u32(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
 
 // Tiled bulk store of one box, and its form that adds (fp32) to memory.
 __device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src, int x, int y, int z) {
