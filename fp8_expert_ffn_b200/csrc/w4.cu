@@ -1,9 +1,12 @@
 // Products with 4-bit expert weights for few rows per expert (decode):
 //   y[r, j] = sum_groups s[g, j, c] * sum_{i in c} x[perm[r], i] (q[g, j, i] - z[g, j, c])
-// and the gate/up form h = silu(gate) * up. A weight is read once for up to 16
-// rows, half a byte each, so HBM bounds the kernel as long as unpacking keeps
-// up: 6.5 TB/s is 46 codes per SM and cycle, which leaves about 45
-// instructions per warp for 512 codes.
+// and the gate/up form h = silu(gate) * up. A weight is read once for up to 8
+// (or 16, see launch_w4) rows, half a byte each, so HBM would bound the kernel
+// if unpacking kept up: 6.5 TB/s is 46 codes per SM and cycle, or 45 issue
+// slots per scheduler for 512 codes, and the kernel takes 38 instructions for
+// them. It runs at 4.35 TB/s (a decode batch of 64 tokens over 257 experts,
+// 1.84 GB: 422 us; without the arithmetic the same copies take 311 us): three
+// warps per scheduler issue 0.55 instructions per cycle.
 //
 // Unpacking is exact and short: code nibbles i and i + 4 of a 32-bit word are
 // masked out together and OR-ed into the mantissas of the 16-bit pair
@@ -16,14 +19,17 @@
 // permutes. tcgen05 would need the unpacked weights back in shared or tensor
 // memory, a second trip per code that the memory-bound case has no use for.
 //
-// Layout: 8 warps per CTA, 2 CTAs per SM, persistent over (group, column tile,
-// rows chunk). A warp owns 64 weight rows (32 gate and 32 up) and a contiguous
-// part of the contraction, and streams its codes through its own ring of TMA
-// boxes (64 rows x 64 bytes = 128 codes, 64-byte swizzle: lane (g, t) reads
-// word t of row g without bank conflicts), so no warp waits for another until
-// a tile's partial sums meet in shared memory, added in warp order. The warps
-// of a CTA split the contraction 8, 4, 2 or 1 ways and the columns by the
-// rest (see launch_w4).
+// Layout: 4 warps per CTA, 3 CTAs per SM, persistent over (group, column tile,
+// rows chunk). A warp owns 64 weight rows (32 gate and 32 up) and every wk-th
+// stage of the contraction, and streams its codes through its own ring of two
+// TMA boxes (64 rows x 128 bytes = 256 codes, 128-byte swizzle: lane (g, t)
+// reads word t of a chunk of row g without bank conflicts), so no warp waits
+// for another until a unit's partial sums meet in shared memory, added in
+// warp order. The warps of a CTA split the contraction 4, 2 or 1 ways and the
+// columns by the rest (see launch_w4). Measured and dropped: 16 warps per SM
+// with 128-code stages (465 against 418 us) and 128 rows per warp (500 against
+// 439), both for their 64-byte boxes; 24 warps of 80 registers (no gain at 64
+// tokens, 102 against 86 us for the down projection).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -404,7 +410,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   // This warp's stages of a unit: every wk-th, so that the warps along the
   // contraction read neighbouring pieces of the same rows at one time.
   const int kb0 = kw, kb1 = p.nkb;
-  // The ring runs STAGES blocks ahead of use, across tiles; every lane keeps
+  // The ring runs STAGES stages ahead of use, across units; every lane keeps
   // its state and one of them issues the copies.
   const uint32_t ring = smem_u32(smem) + warp * (STAGES * STAGE_BYTES);
   uint64_t* bar = s_bar[warp];
@@ -419,11 +425,11 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       i_row = (u.nt * wn + nw) * wrows;
     }
   };
-  auto issue = [&]() {   // the next block, if there is one
+  auto issue = [&]() {   // the next stage, if there is one
     if (i_unit >= total || kb0 >= kb1) return;
     const uint32_t s = issued % STAGES;
     if (issued == withheld) {
-      // test only: this block never arrives
+      // test only: this stage never arrives
     } else if (elect_one()) {
       uint8_t* dst = smem + (warp * STAGES + s) * STAGE_BYTES;
       mbar_arrive_expect_tx(&bar[s], STAGE_BYTES);

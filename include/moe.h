@@ -501,8 +501,9 @@ typedef struct {
 } moe_w4_weights;
 
 /* Matrix-vector products with 4-bit expert weights, for decode batches: the
- * weights of every group that has rows are streamed once per 16 of its rows,
- * so it is meant for a few rows per expert (it is right for any number).
+ * weights of every group that has rows are streamed once per 8 of its rows
+ * (16 where groups have more than 8 on average), so it is meant for a few
+ * rows per expert (it is right for any number).
  *   y[r] = x[perm[r]] w[g]^T   (perm NULL: x[r])
  *   x     [x_rows][ldx] of `type` (MOE_BF16 or MOE_F16), 16-byte aligned,
  *         ldx a multiple of 8; perm [rows] as moe_permute writes it: one
@@ -562,7 +563,8 @@ int moe_kernels_per_forward(moe_layer_t layer, int T);
 /* Test hook for failure detection (library plumbing: no counterpart on the
  * pages). Arms a one-shot stall for the next grouped-GEMM launch on this
  * handle (moe_gate_up, moe_down, or those inside moe_expert_ffn and
- * moe_layer_forward): the first CTA's TMA producer skips its first pipeline
+ * moe_layer_forward; or moe_grouped_mm and its gradients, moe_w4_matvec and
+ * moe_w4_gate_up): the first CTA's TMA producer skips its first pipeline
  * stage, so the MMA issuer's wait for it can never complete, and every
  * pipeline wait of that launch gives up after wait_limit_ns (> 0) instead of
  * the normal 1 s. The kernel then records MOE_STATUS_WAIT_TIMEOUT, every
