@@ -623,7 +623,7 @@ static moe_status w4_call(moe_layer_t L, moe_dtype t, const void* x, int x_rows,
   if (rows == 0) return MOE_OK;
   if (!is_type16(t) || !(y_t == t || y_t == MOE_F32)) return MOE_ERR_INVALID_ARG;
   if (n < 1 || k < 1 || n > kMaxDim || k > kMaxDim || ldx < k || ldx > kMaxLd || ldy < n || ldy > kMaxLd ||
-      x_rows < 1 || x_rows > kMaxT * 9 || !x || !y || !offsets || (!perm && x_rows < rows))
+      rows > kMaxT || x_rows < 1 || x_rows > kMaxT * 9 || !x || !y || !offsets || (!perm && x_rows < rows))
     return MOE_ERR_INVALID_ARG;
   moe_status s = check_w4(w, k);
   if (s == MOE_OK && dual) {

@@ -426,7 +426,8 @@ moe_status moe_combine(moe_layer_t layer, const uint16_t* y, const int32_t* inv,
  *   - NaN and infinities follow IEEE arithmetic and stay in the rows (for
  *     weight gradients: in the groups) that they belong to;
  *   - 1 <= n, k, f <= 65536, row strides at most 2^20 elements, `rows` at
- *     most 9 * 2^20; rows = 0 is a no-op (a weight gradient is still set);
+ *     most 9 * 2^20 (2^20 in the 4-bit calls); rows = 0 is a no-op (a weight
+ *     gradient is still set);
  *   - inputs and outputs must not overlap unless a call says so;
  *   - nothing is allocated and no workspace is used, so calls on different
  *     streams may overlap. */

@@ -105,7 +105,7 @@ def w4(fn="moe_w4_matvec", layer=H, type=B, x=P, x_rows=5, ldx=64, perm=P, codes
 @pytest.mark.parametrize("kw,code", [
     (dict(layer=None), BAD), (dict(rows=-1), BAD), (dict(type=F32), BAD), (dict(y_type=F), BAD), (dict(x=None), BAD),
     (dict(y=None), BAD), (dict(off=None), BAD), (dict(n=0), BAD), (dict(k=0), BAD), (dict(n=65537), BAD),
-    (dict(ldx=56), BAD), (dict(ldy=63), BAD), (dict(x_rows=0), BAD), (dict(perm=None, x_rows=4), BAD),
+    (dict(ldx=56), BAD), (dict(ldy=63), BAD), (dict(x_rows=0), BAD), (dict(rows=(1 << 20) + 1), BAD), (dict(perm=None, x_rows=4), BAD),
     (dict(codes=None), BAD), (dict(scales=None), BAD), (dict(scale_type=3), BAD), (dict(group=16), BAD),
     (dict(group=256), BAD), (dict(ld=16), BAD), (dict(k=65, ldx=72, ld=32), BAD), (dict(ld=65552), BAD),
     (dict(x=P + 8), MIS), (dict(ldx=68), MIS), (dict(codes=P + 8), MIS), (dict(ld=40), MIS), (dict(scales=P + 1), MIS),
