@@ -514,7 +514,9 @@ typedef struct {
  *   y     [rows][ldy] of y_type (`type` or MOE_F32), any stride
  * Codes less zero points are exact in `type`; products are summed in fp32
  * per group of columns and the scale is applied to that sum in fp32. The
- * order of every sum is fixed. The pages describe no such call. */
+ * order of every sum is fixed by the call's sizes (n, k, rows and the layer's
+ * groups), so results do not change from run to run. The pages describe no
+ * such call. */
 moe_status moe_w4_matvec(moe_layer_t layer, moe_dtype type, const void* x, int x_rows, long long ldx,
                          const int32_t* perm, const moe_w4_weights* w, const int32_t* offsets, int rows, int n, int k,
                          moe_dtype y_type, void* y, long long ldy, void* stream);

@@ -678,3 +678,90 @@ def test_calls_go_to_the_current_stream():
         stream.synchronize()
         want = swiglu_reference(g, u)
         assert torch.allclose(h.double(), want, rtol=1e-5, atol=1e-6)
+
+
+# ------------------------------------------------------------ the ends of the ranges
+
+@pytest.mark.parametrize("op", OPS)
+def test_mm_with_256_experts_and_the_shared_one(op):
+    rng = np.random.default_rng(21)
+    counts = rng.integers(0, 9, size=257)
+    counts[[0, 100, 256]] = 0, 70, 300
+    gr = Groups(counts.tolist(), 1, lead=1, tail=1)
+    n, k = 72, 136
+    x = ints(rng, (gr.rows, k), 3) if op != "dgrad" else None
+    dy = ints(rng, (gr.rows, n), 3) if op != "mm" else None
+    w = ints(rng, (gr.G, n, k), 3) if op != "wgrad" else None
+    res = run_mm(op, gr, BF, BF, n, k, x, dy, w, ldo_extra=0)
+    ref, _ = mm_reference(op, gr, x, dy, w)
+    if op != "wgrad":
+        res, ref = res[gr.first:gr.last], ref[gr.first:gr.last]
+    assert torch.equal(res, ref.to(F32).to(BF))
+
+
+@pytest.mark.parametrize("dual", [False, True])
+def test_w4_with_256_experts_and_the_shared_one(dual):
+    rng = np.random.default_rng(22)
+    counts = rng.integers(0, 4, size=257)
+    counts[[0, 77, 256]] = 0, 300, 33
+    gr = Groups(counts.tolist(), 1, lead=1, tail=1)
+    n, k, T = 72, 300, 50
+    a, b = (W4(rng, gr.G, n, k, 32, True, BF, exact=True) for _ in range(2))
+    x, xb, perm = w4_inputs(rng, gr, T, k, BF, True, up8(k))
+    y = out_buffer(gr.rows, n, n, F32)
+    args = (gr.layer, fx.MOE_BF16, xb, T, xb.stride(0), perm)
+    if dual:
+        fx.moe_w4_gate_up(*args, a.desc, b.desc, gr.offsets, gr.rows, n, k, fx.MOE_F32, y, n)
+    else:
+        fx.moe_w4_matvec(*args, a.desc, gr.offsets, gr.rows, n, k, fx.MOE_F32, y, n)
+    status_ok(gr.layer)
+    assert (y[:gr.first] == SENTINEL).all() and (y[gr.last:] == SENTINEL).all()
+    for g, (s, e) in enumerate(gr.spans):
+        xr = x[perm[s:e].long()]
+        ref = xr @ a.dense[g].T
+        if dual:   # both products are exact; silu in fp32: exp and the quotient off by a few 2^-24
+            ref = ref * torch.sigmoid(ref) * (xr @ b.dense[g].T)
+            assert ((y[s:e].double() - ref).abs() <= 16 * 2.0 ** -24 * ref.abs() + 1e-30).all()
+        else:
+            assert torch.equal(y[s:e], ref.to(F32))
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_w4_scales_at_any_element_address(group, zeros):
+    """Scales and zero points that start in the middle of a 16-byte piece."""
+    rng = np.random.default_rng(23)
+    gr = Groups((3, 9), 0)
+    n, k, T = 80, 1024, 4
+    w = W4(rng, gr.G, n, k, group, zeros, BF, exact=True)
+
+    def moved(t):
+        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        buf[1:] = t.view(-1)
+        return buf[1:].view(t.shape)
+
+    desc = fx.W4Weights(w.codes, moved(w.scales), moved(w.zeros) if zeros else None, fx.MOE_BF16, group)
+    x, xb, perm = w4_inputs(rng, gr, T, k, BF, True, k)
+    y = torch.empty(gr.rows, n, dtype=F32, device="cuda")
+    fx.moe_w4_matvec(gr.layer, fx.MOE_BF16, xb, T, k, perm, desc, gr.offsets, gr.rows, n, k, fx.MOE_F32, y, n)
+    status_ok(gr.layer)
+    for g, (s, e) in enumerate(gr.spans):
+        assert torch.equal(y[s:e], (x[perm[s:e].long()] @ w.dense[g].T).to(F32))
+
+
+@pytest.mark.parametrize("n,k", [(1024, 1536), (100, 2048)])
+def test_w4_gate_up_does_not_depend_on_the_batch(n, k):
+    """A row's bits alone and among others in batches whose sizes split the
+    contraction the same way."""
+    rng = np.random.default_rng(24)
+    gr = Groups((5, 0, 6), 0)
+    a, b = (W4(rng, gr.G, n, k, 128, False, BF, exact=False) for _ in range(2))
+    x, xb, perm = w4_inputs(rng, gr, 11, k, BF, False, k)
+    call = lambda off, out: fx.moe_w4_gate_up(gr.layer, fx.MOE_BF16, xb, 11, k, None, a.desc, b.desc, off, gr.rows,  # noqa: E731
+                                              n, k, fx.MOE_BF16, out, n)
+    y, again, part = (out_buffer(gr.rows, n, n, BF) for _ in range(3))
+    call(gr.offsets, y)
+    call(gr.offsets, again)
+    assert torch.equal(y.view(torch.int16), again.view(torch.int16))
+    call(torch.tensor([0, 5, 5, 6, 6], dtype=torch.int32, device="cuda"), part)   # group 2 holds row 5 alone
+    assert torch.equal(part[:6].view(torch.int16), y[:6].view(torch.int16)) and (part[6:] == SENTINEL).all()
