@@ -635,17 +635,18 @@ cudaError_t launch_w4(const moe_layer_s* L, moe_dtype t, const void* x, int x_ro
   // Warps along the contraction. More of them give more, smaller units (the
   // only way to fill the machine with few experts), fewer leave more stages
   // per unit to pay for its fixed cost (finding it, joining the partial sums:
-  // half a stage's time). The split with the least expected time of a CTA,
+  // 0.4 of a stage's time). The split with the least expected time of a CTA,
   // from the groups that evenly spread rows would touch: 4 ways for one token
   // or one matrix (30.7 us against 34.8 two ways and 53 one way), 2 ways for
-  // a decode batch of 64 (422 against 430 one way and 463 four ways).
+  // a decode batch of 64 (422 against 430 one way and 463 four ways) and for
+  // the down projection of 16 tokens (78 against 84 and 92).
   const double ctas = double(CTAS_PER_SM) * L->num_sms;
   const double touched = G * (1.0 - exp(-double(rows) / G)) + double(rows) / (16 * nt);
   double best = 0.0;
   for (int wk = WARPS; wk >= 1; wk /= 2) {
     const int cols = (WARPS / wk) * (p.dual ? BOX_ROWS / 2 : BOX_ROWS);
     const double rounds = (touched < double(groups) ? touched : double(groups)) * ((n + cols - 1) / cols) / ctas + 0.5;
-    const double cost = (rounds > 1.0 ? rounds : 1.0) * (2 * ((p.nkb + wk - 1) / wk) + 1);
+    const double cost = (rounds > 1.0 ? rounds : 1.0) * (2 * ((p.nkb + wk - 1) / wk) + 0.8);
     if (best == 0.0 || cost < best) {
       best = cost;
       p.wk = wk;
