@@ -9,9 +9,8 @@ namespace moe {
 
 constexpr int kMaxGroups = 257;   // 256 routed experts and the shared one
 
-// mbar_wait that reads the clock only now and then: the expert operators'
-// roles wait on every stage, often for a fraction of a microsecond, which one
-// read of the global timer already takes. Same limit, abort flag and status.
+// mbar_wait for the expert operators' stages: looks at the abort flag and the
+// clock only every 32nd poll. Same limit, abort flag and status.
 __device__ __forceinline__ bool mbar_wait_stage(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status,
                                                 unsigned long long limit_ns) {
   const uint32_t a = smem_u32(bar);
