@@ -4,14 +4,22 @@
 // Both are bound by HBM (3 and 5 streams of the operands, 6 with h again; no
 // reuse): one 16-byte vector of each operand per thread and trip, 4 CTAs of
 // 256 threads per SM (the gradient over 36,864 rows of 1,536 in bf16, 566 MB:
-// 94 us, 6.0 TB/s; with 6 CTAs 102 us, with two vectors in flight per thread
-// 131 us for the registers they take). 1 - s is formed as exp(-|g|) s or s
-// itself, without the cancellation at large |g|.
+// 94 to 97 us back to back, 5.8 to 6.0 TB/s; with 6 CTAs 8 us more, with two
+// vectors in flight per thread 37 for the registers they take).
+//
+// The arithmetic is silu.cuh's. Its short form holds for gates from kLowGate
+// on with a product dh u inside fp32; a vector with others is noticed here
+// and done again by careful_elements (3 to 6 of the 97 us are the notice; a
+// branch per element in its place took 115 us in all).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cfloat>
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
+#include "silu.cuh"
 
 namespace moe {
 
@@ -43,21 +51,6 @@ template <typename T, int N>
 struct alignas(sizeof(T) * N) Vec {
   T v[N];
 };
-
-// s = 1 / (1 + exp(-g)) and c = 1 - s. For 16-bit types by the special
-// function unit's exponential and reciprocal: their error, at most
-// (|g| + 4) 2^-23 of s, is below a hundredth of the outputs' rounding where s
-// is not negligible, and the IEEE forms (20 instructions more per element)
-// would bound the kernel in place of HBM. NaN stays NaN in both.
-template <bool FAST>
-__device__ __forceinline__ void sigmoid_pair(float g, float& s, float& c) {
-  const float a = fabsf(g);   // exp(-|g|) is in (0, 1]: no overflow on either side
-  const float e = FAST ? ex2_approx(-1.4426950408889634f * a) : expf(-a);
-  const float r = FAST ? rcp_approx(1.0f + e) : 1.0f / (1.0f + e);
-  const float er = e * r;
-  s = g < 0.0f ? er : r;
-  c = g < 0.0f ? r : er;
-}
 
 struct SwigluArgs {
   const void* dh;
@@ -93,6 +86,27 @@ __device__ __forceinline__ bool group_rows(const SwigluArgs& p, int& r0, int& r1
   return true;
 }
 
+// N elements from (row, c) on, one by one from memory (in registers, the
+// second copy of the arithmetic would spill): right for all values.
+template <typename T, int N, bool BACKWARD>
+__device__ __forceinline__ void careful_elements(const SwigluArgs& p, size_t row, int c) {
+  constexpr bool FAST = sizeof(T) == 2;
+#pragma unroll 1
+  for (int j = c; j < c + N; ++j) {
+    const float g = Cvt<T>::to(static_cast<const T*>(p.gate)[row * p.ld_gate + j]);
+    const float u = Cvt<T>::to(static_cast<const T*>(p.up)[row * p.ld_up + j]);
+    const T h = Cvt<T>::from(silu_mul<FAST>(g, u));
+    if (BACKWARD) {
+      const float d = Cvt<T>::to(static_cast<const T*>(p.dh)[row * p.ld_dh + j]);
+      static_cast<T*>(p.o0)[row * p.ld0 + j] = Cvt<T>::from(dgate_mul<FAST>(g, u, d));
+      static_cast<T*>(p.o1)[row * p.ld1 + j] = Cvt<T>::from(silu_mul<FAST>(g, d));
+      if (p.o2) static_cast<T*>(p.o2)[row * p.ld2 + j] = h;
+    } else {
+      static_cast<T*>(p.o0)[row * p.ld0 + j] = h;
+    }
+  }
+}
+
 template <typename T, int N, bool BACKWARD>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) swiglu_kernel(const SwigluArgs p) {
   pdl_wait();
@@ -101,6 +115,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) swiglu_kernel(const Swig
   if (!group_rows(p, r0, r1)) return;
   using V = Vec<T, N>;
   constexpr bool FAST = sizeof(T) == 2;
+  // fp16: below kLowGate every result is zero, and products stay inside fp32
+  constexpr bool RANGE = !std::is_same<T, __half>::value;
   const uint32_t per_row = uint32_t(p.f / N);   // the host picks N = 1 unless it divides f
   const uint64_t total = uint64_t(r1 - r0) * per_row;
   const uint64_t step = uint64_t(gridDim.x) * THREADS;
@@ -113,18 +129,26 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) swiglu_kernel(const Swig
     const V u = *reinterpret_cast<const V*>(static_cast<const T*>(p.up) + row * p.ld_up + c);
     V a, b, d, h;
     if (BACKWARD) d = *reinterpret_cast<const V*>(static_cast<const T*>(p.dh) + row * p.ld_dh + c);
+    bool rare = false;   // a gate below kLowGate, or a product dh u beyond fp32
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const float gv = Cvt<T>::to(g.v[j]), uv = Cvt<T>::to(u.v[j]);
+      rare |= RANGE && gv < kLowGate;
       float s, m;
       sigmoid_pair<FAST>(gv, s, m);
       const float silu = gv * s;
       h.v[j] = Cvt<T>::from(silu * uv);
       if (BACKWARD) {
         const float dv = Cvt<T>::to(d.v[j]);
-        a.v[j] = Cvt<T>::from(dv * uv * (s + silu * m));
+        const float du = dv * uv;
+        rare |= RANGE && fabsf(du) > FLT_MAX;
+        a.v[j] = Cvt<T>::from(du * (s + silu * m));
         b.v[j] = Cvt<T>::from(dv * silu);
       }
+    }
+    if (rare) {
+      careful_elements<T, N, BACKWARD>(p, row, c);
+      continue;
     }
     if (BACKWARD) {
       *reinterpret_cast<V*>(static_cast<T*>(p.o0) + row * p.ld0 + c) = a;

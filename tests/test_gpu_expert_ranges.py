@@ -1,0 +1,84 @@
+"""The expert operators at the ends of their types' ranges, against float64:
+gates so low that exp(gate) is subnormal or zero in fp32 while the result is
+a normal number of its type.
+
+Each tolerance is the arithmetic's own bound, derived beside it."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import fp8_expert_ffn_b200 as fx  # noqa: E402
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+CODE = {BF: fx.MOE_BF16, HF: fx.MOE_F16, F32: fx.MOE_F32}
+
+
+def make_layer(E):
+    router = torch.zeros(E, 128, dtype=F32, device="cuda")
+    return fx.MoeLayer(128, E, 1, 1, fx.LayerWeights(*[None] * 6, router), n_shared=0)
+
+
+def status_ok(layer):
+    code, bits = fx.moe_get_device_status(layer)
+    assert code == fx.MOE_OK, hex(bits)
+
+
+def rounding(dt, want):
+    """Half a step of the type at `want`, its subnormals included, plus the
+    same of fp32 below its normal numbers (products on the way)."""
+    info = torch.finfo(dt)
+    return info.eps / 2 * want.abs() + info.smallest_normal * info.eps / 2 + 2.0 ** -147
+
+
+LOW_GATES = [-1.0, -40.0, -79.5, -80.0, -80.5, -87.0, -87.5, -88.0, -90.0, -91.0, -96.0, -103.0, -104.0, -120.0, -150.0,
+             -172.0, -178.0, -184.0, -300.0, 60.0, 88.0, 100.0]
+
+
+@pytest.mark.parametrize("dt", [BF, HF, F32])
+@pytest.mark.parametrize("pad", [0, 1])   # rows of 16-byte vectors, and element by element
+def test_swiglu_low_gates_and_large_factors(dt, pad):
+    """silu(-88) is a normal number of bf16 and fp32, and a large up or dh
+    brings far lower gates back into the range. The product of dh and up may
+    leave the range where the gradient does not."""
+    top = {BF: 3e38, HF: 6e4, F32: 3e38}[dt]
+    factors = [1.0, -1.5, top, 0.5 * top ** 0.5, -top ** 0.5, 1e-5, top ** -0.5, 0.0]
+    cases = [(g, u, d) for g in LOW_GATES for u in factors for d in factors]
+    f = 64
+    cases += [(0.0, 0.0, 0.0)] * (-len(cases) % f)
+    v = torch.tensor(cases, dtype=torch.float64, device="cuda").T.reshape(3, -1, f)
+    rows, ld = v.shape[1], f + pad
+    buf = torch.zeros(3, rows, ld, dtype=dt, device="cuda")
+    buf[:, :, :f] = v.to(dt)
+    L, t = make_layer(1), CODE[dt]
+    h, dg, du, h2 = (torch.empty(rows, ld, dtype=dt, device="cuda") for _ in range(4))
+    g_, u_, d_ = buf[0], buf[1], buf[2]
+    fx.moe_swiglu(L, t, g_, ld, u_, ld, None, rows, f, h, ld)
+    fx.moe_swiglu_backward(L, t, d_, ld, g_, ld, u_, ld, None, rows, f, dg, ld, du, ld, h2, ld)
+    status_ok(L)
+    g, u, d = (b[:, :f].double() for b in buf)
+    s, c = torch.sigmoid(g), torch.sigmoid(-g)
+    slope = s * (1 + g * c)
+    # exp: (|g| + 8) 2^-23 (the argument's rounding and the function's few
+    # units), at most eight roundings of 2^-24 behind it; below -174 half the
+    # exponential's argument leaves fp32's normal numbers too: two units of
+    # 2^-149 in each of the two factors exp(g / 2) and one in a product with
+    # them. The slope's 1 + g c cancels near its root, so its bound counts
+    # both terms.
+    rel = (g.abs() + 16) * 2.0 ** -23 + 5 * 2.0 ** -149 / torch.exp(g.clamp(min=-205, max=0) / 2)
+    for name, got, want, mag in (("h", h, g * s * u, None), ("h again", h2, g * s * u, None), ("dup", du, d * g * s, None),
+                                 ("dgate", dg, d * u * slope, (d * u).abs() * s * (1 + g.abs() * c))):
+        got = got[:, :f].double()
+        tol = rel * (want.abs() if mag is None else mag) + rounding(dt, want)
+        # results at the type's top may round to infinity
+        far = want.abs() > torch.finfo(dt).max * (1 - 2.0 ** -7)
+        assert not torch.isnan(got).any(), name
+        bad = ((got - want).abs() > tol) & ~far
+        assert not bad.any(), (name, [(g[i].item(), u[i].item(), d[i].item(), got[i].item(), want[i].item())
+                                      for i in map(tuple, bad.nonzero()[:4].tolist())])
+        assert (got[far].abs() >= torch.finfo(dt).max * (1 - 2.0 ** -6)).all(), name
+    assert torch.equal(h.view(torch.uint8)[:, :f], h2.view(torch.uint8)[:, :f])
