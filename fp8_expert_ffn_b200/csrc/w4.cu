@@ -40,6 +40,7 @@
 #include "groups.cuh"
 #include "internal.h"
 #include "pair.cuh"
+#include "silu.cuh"
 
 namespace moe {
 
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
             for (int q = 0; q < p.wk; ++q) a += src[q * (RED_ROWS * 8)];
             if (p.dual) {
               for (int q = 0; q < p.wk; ++q) b += src[q * (RED_ROWS * 8) + 128];
-              a = a / (1.0f + expf(-a)) * b;
+              a = silu_mul<false>(a, b);
             }
             store_y(p, size_t(u.r0 + 8 * j + r) * size_t(p.ldy) + size_t(col), a);
           }

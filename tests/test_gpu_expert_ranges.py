@@ -82,3 +82,41 @@ def test_swiglu_low_gates_and_large_factors(dt, pad):
                                       for i in map(tuple, bad.nonzero()[:4].tolist())])
         assert (got[far].abs() >= torch.finfo(dt).max * (1 - 2.0 ** -6)).all(), name
     assert torch.equal(h.view(torch.uint8)[:, :f], h2.view(torch.uint8)[:, :f])
+
+
+@pytest.mark.parametrize("dt,out_dt", [(BF, BF), (HF, F32), (BF, F32)])
+def test_w4_gate_up_low_gates(dt, out_dt):
+    """The gate/up form's activation where exp(-gate) is beyond fp32: one
+    column of weights, so that both products are exact."""
+    gates = [-40.0, -80.5, -87.5, -88.75, -90.0, -91.5, -96.0, -104.0, -130.0, -172.0, -400.0, 90.0]
+    ups = [1.0, -3.0, 1e20, -3e38]
+    n, k = len(gates) * len(ups), 32
+    gate_scale = torch.tensor([abs(g) / 7 for g in gates for _ in ups], dtype=torch.float64)
+    up_scale = torch.tensor([abs(u) for _ in gates for u in ups], dtype=torch.float64)
+    negative = torch.tensor([g < 0 for g in gates for _ in ups])
+    down = torch.tensor([u < 0 for _ in gates for u in ups])
+
+    def weights(scale, code):
+        codes = torch.zeros(1, n, 16, dtype=torch.uint8)
+        codes[0, :, 0] = code
+        return fx.W4Weights(codes.cuda(), scale.to(F32).view(1, n, 1).cuda(), None, fx.MOE_F32, 32)
+
+    gate, up = weights(gate_scale, torch.where(negative, 1, 15)), weights(up_scale, torch.where(down, 7, 9))
+    x = torch.zeros(1, k, dtype=dt, device="cuda")
+    x[0, 0] = 1
+    L = make_layer(1)
+    offsets = torch.tensor([0, 1, 1], dtype=torch.int32, device="cuda")
+    h = torch.empty(1, n, dtype=out_dt, device="cuda")
+    fx.moe_w4_gate_up(L, CODE[dt], x, 1, k, None, gate, up, offsets, 1, n, k, CODE[out_dt], h, n)
+    status_ok(L)
+    sign = lambda neg: torch.where(neg, -1.0, 1.0).double()  # noqa: E731
+    g = (7 * gate_scale.to(F32)).double().cuda() * sign(negative).cuda()    # one fp32 rounding each
+    u = up_scale.to(F32).double().cuda() * sign(down).cuda()
+    want = g * torch.sigmoid(g) * u
+    # as for silu in fp32, and the rounding of g in exp(g): |g| 2^-24 once more
+    rel = (2 * g.abs() + 16) * 2.0 ** -23 + 5 * 2.0 ** -149 / torch.exp(g.clamp(min=-205, max=0) / 2)
+    tol = rel * want.abs() + rounding(out_dt, want)
+    got, far = h[0].double(), want.abs() > torch.finfo(out_dt).max * (1 - 2.0 ** -7)
+    bad = ~((got - want).abs() <= tol) & ~far
+    assert not bad.any(), [(g[i].item(), u[i].item(), got[i].item(), want[i].item()) for i in bad.nonzero()[:, 0].tolist()]
+    assert (got[far].abs() >= torch.finfo(out_dt).max * (1 - 2.0 ** -6)).all()
