@@ -243,9 +243,13 @@ __device__ __forceinline__ void load_scales(const W4Args& p, const void* sp, con
     } else {
 #pragma unroll
       for (int q = 0; q < GPS; ++q) {
-        const int at = srow[h] + min(g0 + q, p.ng - 1);   // groups past the row's end meet zero x
-        o.raw[h][q] = p.scale_type == MOE_F32 ? ldg32(static_cast<const uint32_t*>(sp) + at)
-                                              : ldg16(static_cast<const uint16_t*>(sp) + at);
+        // groups past the row's end meet zero x: their scale is zero (an
+        // infinite one would make them NaN)
+        const int at = srow[h] + g0 + q;
+        o.raw[h][q] = 0u;
+        if (g0 + q < p.ng)
+          o.raw[h][q] = p.scale_type == MOE_F32 ? ldg32(static_cast<const uint32_t*>(sp) + at)
+                                                : ldg16(static_cast<const uint16_t*>(sp) + at);
       }
       if (ZEROS) {
 #pragma unroll

@@ -120,3 +120,29 @@ def test_w4_gate_up_low_gates(dt, out_dt):
     bad = ~((got - want).abs() <= tol) & ~far
     assert not bad.any(), [(g[i].item(), u[i].item(), got[i].item(), want[i].item()) for i in bad.nonzero()[:, 0].tolist()]
     assert (got[far].abs() >= torch.finfo(out_dt).max * (1 - 2.0 ** -6)).all()
+
+
+@pytest.mark.parametrize("scale_dt", [BF, HF, F32])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group,k", [(32, 33), (32, 1), (64, 65), (64, 300), (128, 129), (128, 1024 + 40)])
+def test_w4_infinite_last_scale(group, k, zeros, scale_dt):
+    """An infinite scale of a row's last columns makes the row infinite, not
+    NaN: columns past the row's end have no scale."""
+    n, T = 40, 3
+    ng, ld = -(-k // group), -(-((k + 1) // 2) // 16) * 16
+    codes = torch.full((1, n, ld), 0x99, dtype=torch.uint8, device="cuda")       # 1 above the zero point
+    scales = torch.ones(1, n, ng, dtype=scale_dt, device="cuda")
+    scales[0, ::2, -1] = float("inf")
+    zp = torch.full((1, n, ng), 8, dtype=torch.uint8, device="cuda") if zeros else None
+    w = fx.W4Weights(codes, scales, zp, CODE[scale_dt], group)
+    ldx = (k + 7) // 8 * 8
+    x = torch.full((T, ldx), float("nan"), dtype=BF, device="cuda")
+    x[:, :k] = torch.tensor([1.0, -1.0, 2.0], device="cuda")[:, None]
+    L = make_layer(1)
+    offsets = torch.tensor([0, T, T], dtype=torch.int32, device="cuda")
+    y = torch.empty(T, n, dtype=F32, device="cuda")
+    fx.moe_w4_matvec(L, fx.MOE_BF16, x, T, ldx, None, w, offsets, T, n, k, fx.MOE_F32, y, n)
+    status_ok(L)
+    want = x[:, :1].float() * k * torch.ones(1, n, device="cuda")
+    want[:, ::2] *= float("inf")
+    assert torch.equal(y, want)
