@@ -18,8 +18,7 @@
 // MN-major over the group's rows. A wgrad block that passes the group's end
 // has zeros copied over the rows past it in shared memory before the MMA (in
 // both operands, so that a NaN there is not multiplied by zero; by bulk
-// copies, which like the loads need no cluster-scope fences: with stores and
-// such fences a tile with a tail waited 4 thousand cycles for them).
+// copies: with plain stores a tile with a tail waited 4 thousand cycles).
 //
 // Kernel layout: CTA pairs (cluster of 2, tcgen05 cta_group::2, M 256 x N up
 // to 256 x K 16 per instruction), persistent over a device-side tile list.
@@ -28,8 +27,7 @@
 // independent 128 x 256 tiles would move 48 KB.
 //   warp 0      TMA producer into a ring of 6 stages (16 KB of A, up to 16 KB of B)
 //   warp 1      TMEM allocation; in the leading CTA the MMA issuer
-//   warp 2      relay: waits for its CTA's copies, clears a wgrad tail, and
-//               signals the leading CTA
+//   warp 2      wgrad: clears its CTA's half of a tail
 //   warp 3      idle
 //   warps 4-11  epilogue, two warpgroups with 128 output rows each: TMEM lanes
 //               32*(w%4).., one output column per lane; two 256-column TMEM
@@ -41,6 +39,15 @@
 // 1536 x 5120: 400 us, 1.45 PFLOP/s; one group of as many rows 354 us where
 // cuBLAS takes 342), HBM below (one decode step of 65 experts: 184 us,
 // 5.6 TB/s).
+// Hand-over between the CTAs: the leading CTA's MMA reads stages that lie in
+// the other one, so both CTAs' copies complete on the leading CTA's barrier
+// (the cta_group::2 form of the loads; a completion releases what its copy
+// wrote at cluster scope), where each CTA has announced its own. Only a wgrad
+// tail completes on its CTA's own barrier, and that CTA arrives on the leading
+// one's when the zeros lie. Waits on barriers that the other CTA signals
+// acquire, and arrivals by threads release, at cluster scope. One thread per
+// warpgroup hands an accumulator back: a release by each warp cost the wgrad
+// over 512 rows per group 2 of its 101 us.
 // No TMA multicast; commits signal both CTAs. Every wait is bounded (1 s): on
 // a timeout the status word is set, all roles leave, copies in flight are
 // waited for (bounded) and the TMEM is released.
@@ -271,8 +278,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
   constexpr int STAGES = stages(BR, PROMOTE), STAGE_BYTES = stage_bytes(BR);
   constexpr int THREADS = threads(BR, PROMOTE), EPI_WARPS = epi_warps(BR, PROMOTE);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full_bar[STAGES];    // this CTA's copies of a stage
-  __shared__ __align__(8) uint64_t ready_bar[STAGES];   // leading CTA: both CTAs' stages complete
+  __shared__ __align__(8) uint64_t full_bar[STAGES];    // leading CTA: both CTAs' parts of a stage
+  __shared__ __align__(8) uint64_t tail_bar[STAGES];    // wgrad: this CTA's copies of a group's last block
   __shared__ __align__(8) uint64_t empty_bar[STAGES];
   __shared__ __align__(8) uint64_t tfull_bar[2];
   __shared__ __align__(8) uint64_t tempty_bar[2];       // leading CTA: both CTAs' epilogues
@@ -281,7 +288,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
   __shared__ TileList s_tiles;
   __shared__ uint32_t tmem_base_s;
   __shared__ int s_abort_store;
-  __shared__ uint32_t s_relayed, s_issued, s_withheld;
+  __shared__ uint32_t s_issued, s_withheld, s_drain;
+  __shared__ uint32_t s_tails, s_tail_phase;   // a bit per slot: its last stage was a tail; parity of its last tail
+  __shared__ uint32_t s_progress_store;        // stages issued so far, by tiles
+  volatile uint32_t* s_progress = &s_progress_store;
   volatile int* s_abort = &s_abort_store;
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -291,19 +301,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full_bar[s], 1);
-      mbar_init(&ready_bar[s], 2);
+      mbar_init(&full_bar[s], 2);
+      mbar_init(&tail_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull_bar[b], 1);
-      mbar_init(&tempty_bar[b], 2 * EPI_WARPS);
+      mbar_init(&tempty_bar[b], 2 * (EPI_WARPS / 4));
     }
     mbar_init(&done_bar, 1);
     mbar_init(&zero_bar, 1);
     s_abort_store = 0;
-    s_relayed = 0;
     s_issued = 0;
+    s_drain = 0;
+    s_tails = 0;
+    s_tail_phase = 0;
+    s_progress_store = 0;
     s_withheld = 0xFFFFFFFFu;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -331,7 +344,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
   if (warp == 0) {
     // -------------------------------------------------------------- producer
     if (elect_one()) {
-      uint32_t it = 0;
+      const uint32_t full = map_rank(full_bar, 0);
+      uint32_t it = 0, tails = 0, tail_next = 0;
       bool ok = true;
       for (int w = 0, i; ok && (i = tile_at(w, pair, npairs)) < total; ++w) {
         const Tile t = decode_tile<MODE, BR>(i, s_tiles, p);
@@ -339,9 +353,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
         const int acol = t.col0 + int(rank) * 128;
         const int brow = t.row0 + int(rank) * half;
         const uint32_t bytes = A_BYTES + (B_MN ? ((half + 63) >> 6) * BOX_BYTES : half * BK * 2);
+        const bool ragged = MODE == MOE_MM_WGRAD && (s_tiles.plan.off[t.g + 1] - t.r_first) % BK != 0;
         for (int kb = 0; kb < t.nk; ++kb) {
           const int s = it % STAGES;
-          if (!mbar_wait_stage(&empty_bar[s], ((it / STAGES) & 1u) ^ 1u, s_abort, p.status, p.wait_ns)) { ok = false; break; }
+          if (!mbar_wait_stage<true>(&empty_bar[s], ((it / STAGES) & 1u) ^ 1u, s_abort, p.status, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          // the stage's copies complete on the leading CTA's barrier, or,
+          // where zeros have to follow them, on this CTA's own
+          const bool tail = ragged && kb == t.nk - 1;
+          if (MODE == MOE_MM_WGRAD) tails = tail ? tails | (1u << s) : tails & ~(1u << s);
           if (p.withhold && blockIdx.x == 0 && it == 0) {   // test only: this stage never arrives
             s_withheld = it++;
             continue;
@@ -349,33 +371,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
           uint8_t* a = smem + s * STAGE_BYTES;
           uint8_t* b = a + A_BYTES;
           const int k0 = (MODE == MOE_MM_WGRAD ? t.r_first : 0) + kb * BK;
-          mbar_arrive_expect_tx(&full_bar[s], bytes);
-          if (MODE == MOE_MM_FORWARD) {
-            tma_load_3d(a, &tmA, &full_bar[s], k0, acol, t.g);
-          } else if (MODE == MOE_MM_DGRAD) {
-            tma_load_3d(a, &tmA, &full_bar[s], acol, k0, t.g);
-            tma_load_3d(a + BOX_BYTES, &tmA, &full_bar[s], acol + 64, k0, t.g);
+          const uint32_t fb = full + s * 8;
+          if (MODE == MOE_MM_WGRAD) {
+            uint32_t bar = fb;
+            if (tail) {
+              bar = smem_u32(&tail_bar[s]);
+              mbar_arrive_expect_tx(&tail_bar[s], bytes);
+              tail_next ^= 1u << s;
+            } else {
+              mbar_expect_pair(fb, bytes);
+            }
+            tma_load_2d_pair(a, &tmA, bar, acol, k0);
+            tma_load_2d_pair(a + BOX_BYTES, &tmA, bar, acol + 64, k0);
+            for (int c = 0; c < half; c += 64) tma_load_2d_pair(b + c * (BK * 2), &tmB.m[0], bar, brow + c, k0);
           } else {
-            tma_load_2d(a, &tmA, &full_bar[s], acol, k0);
-            tma_load_2d(a + BOX_BYTES, &tmA, &full_bar[s], acol + 64, k0);
-          }
-          if (B_MN) {
-            for (int c = 0; c < half; c += 64) tma_load_2d(b + c * (BK * 2), &tmB.m[0], &full_bar[s], brow + c, k0);
-          } else {
+            mbar_expect_pair(fb, bytes);
+            if (MODE == MOE_MM_FORWARD) {
+              tma_load_3d_pair(a, &tmA, fb, k0, acol, t.g);
+            } else {
+              tma_load_3d_pair(a, &tmA, fb, acol, k0, t.g);
+              tma_load_3d_pair(a + BOX_BYTES, &tmA, fb, acol + 64, k0, t.g);
+            }
             int r = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {   // 128, 64, 32, 16 rows: half is a multiple of 16, 128 at most
               const int h = 128 >> j;
               if (half & h) {
-                tma_load_2d(b + r * (BK * 2), &tmB.m[j], &full_bar[s], k0, brow + r);
+                tma_load_2d_pair(b + r * (BK * 2), &tmB.m[j], fb, k0, brow + r);
                 r += h;
               }
             }
           }
           ++it;
         }
+        if (MODE == MOE_MM_WGRAD) *s_progress = it;
       }
       s_issued = it;
+      s_tails = tails;
+      s_tail_phase = ~tail_next;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -390,13 +423,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
           const int part = PROMOTE ? kb % SEGMENT : kb;   // K block within the accumulator's sum
           const uint32_t buf = tb & 1u;
           if (part == 0 &&
-              !mbar_wait_stage(&tempty_bar[buf], ((tb >> 1) & 1u) ^ 1u, s_abort, p.status, p.wait_ns)) {
+              !mbar_wait_stage<true>(&tempty_bar[buf], ((tb >> 1) & 1u) ^ 1u, s_abort, p.status, p.wait_ns)) {
             ok = false;
             break;
           }
           const uint32_t d = tmem_base + buf * TMEM_BUF;
           const int s = it % STAGES;
-          if (!mbar_wait_stage(&ready_bar[s], (it / STAGES) & 1u, s_abort, p.status, p.wait_ns)) { ok = false; break; }
+          if (!mbar_wait_stage<true>(&full_bar[s], (it / STAGES) & 1u, s_abort, p.status, p.wait_ns)) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
           const uint32_t a_addr = smem_u32(smem + s * STAGE_BYTES);
           const uint64_t ad = A_MN ? smem_desc_mn_sw128(a_addr, BOX_BYTES) : smem_desc_sw128(a_addr);
@@ -419,73 +455,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
       int never = 0;
       mbar_wait_stage(&done_bar, 0, &never, p.status, p.wait_ns);
     }
-  } else if (warp == 2) {
-    // ----------------------------------------------------------------- relay
+  } else if (MODE == MOE_MM_WGRAD && warp == 2) {
+    // ----------------------------------------------------------------- tails
     uint8_t* zeros = smem + STAGES * STAGE_BYTES + 2 * STG_BYTES;
-    uint32_t zero_phase = 0;
-    if (MODE == MOE_MM_WGRAD) {
-      for (int v = lane; v < BOX_BYTES / 16; v += 32) reinterpret_cast<uint4*>(zeros)[v] = make_uint4(0u, 0u, 0u, 0u);
-      fence_proxy_async_smem();
-      __syncwarp();
-    }
-    uint32_t it = 0;
-    bool ok = true;
-    for (int w = 0, i; ok && (i = tile_at(w, pair, npairs)) < total; ++w) {
+    for (int v = lane; v < BOX_BYTES / 16; v += 32) reinterpret_cast<uint4*>(zeros)[v] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+    __syncwarp();
+    const uint32_t full = map_rank(full_bar, 0);
+    uint32_t it = 0, phase = 0, zero_phase = 0;
+    for (int w = 0, i; (i = tile_at(w, pair, npairs)) < total; ++w) {
       const Tile t = decode_tile<MODE, BR>(i, s_tiles, p);
-      int left = 0;   // wgrad: the group's rows from the current block on
-      if (MODE == MOE_MM_WGRAD) left = s_tiles.plan.off[t.g + 1] - t.r_first;
-      for (int kb = 0; kb < t.nk; ++kb) {
-        const int s = it % STAGES;
-        const bool got = mbar_wait_stage(&full_bar[s], (it / STAGES) & 1u, s_abort, p.status, p.wait_ns);
-        if (!__all_sync(0xFFFFFFFFu, got)) { ok = false; break; }
-        if (MODE == MOE_MM_WGRAD) {
-          if (left < BK) {
-            // rows [left, 64) of every box belong to the next group (or lie
-            // past the last row): zeros are copied over them
-            if (elect_one()) {
-              const int boxes = 2 + ((tile_n(t) / 2 + 63) >> 6);
-              const uint32_t bytes = uint32_t(BK - left) * 128u;
-              mbar_arrive_expect_tx(&zero_bar, boxes * bytes);
-              for (int bx = 0; bx < boxes; ++bx)
-                bulk_copy_smem(smem + s * STAGE_BYTES + bx * BOX_BYTES + left * 128, zeros, bytes, &zero_bar);
-            }
-            __syncwarp();
-            const bool clean = mbar_wait_stage(&zero_bar, zero_phase, s_abort, p.status, p.wait_ns);
-            zero_phase ^= 1u;
-            if (!__all_sync(0xFFFFFFFFu, clean)) {
-              // the copies must land before the CTA ends
-              int never = 0;
-              mbar_wait_stage(&zero_bar, zero_phase ^ 1u, &never, p.status, p.wait_ns);
-              ok = false;
-              break;
-            }
-          }
-          left -= BK;
-        }
-        if (lane == 0) mbar_arrive_rank(&ready_bar[s], 0);
-        ++it;
+      it += t.nk;
+      const int left = (s_tiles.plan.off[t.g + 1] - t.r_first) % BK;   // the last block's rows, if not all are
+      if (left == 0) continue;
+      const int s = (it - 1) % STAGES;
+      // many tiles may pass before this one: the limit counts from the last stage issued
+      const bool got =
+          mbar_wait_stage(&tail_bar[s], (phase >> s) & 1u, s_abort, p.status, p.wait_ns, s_progress);
+      if (!__all_sync(0xFFFFFFFFu, got)) break;
+      phase ^= 1u << s;
+      // rows [left, 64) of every box belong to the next group (or lie past
+      // the last row): zeros are copied over them
+      if (elect_one()) {
+        const int boxes = 2 + ((tile_n(t) / 2 + 63) >> 6);
+        const uint32_t bytes = uint32_t(BK - left) * 128u;
+        mbar_arrive_expect_tx(&zero_bar, boxes * bytes);
+        for (int bx = 0; bx < boxes; ++bx)
+          bulk_copy_smem(smem + s * STAGE_BYTES + bx * BOX_BYTES + left * 128, zeros, bytes, &zero_bar);
       }
+      __syncwarp();
+      const bool clean = mbar_wait_stage(&zero_bar, zero_phase, s_abort, p.status, p.wait_ns);
+      if (!__all_sync(0xFFFFFFFFu, clean)) {
+        int never = 0;   // the copies must land before the CTA ends
+        mbar_wait_stage(&zero_bar, zero_phase, &never, p.status, p.wait_ns);
+        break;
+      }
+      zero_phase ^= 1u;
+      if (lane == 0) mbar_arrive_pair(full + s * 8);
     }
-    if (lane == 0) s_relayed = it;
   }
   // ------------------------------------------------ teardown (warps 0 to 3)
   __syncwarp();
   asm volatile("bar.sync 0;" ::: "memory");
-  if (warp == 0 && lane == 0) {
-    // copies issued but never relayed (only after an abort) must land first
-    int never = 0;
-    for (uint32_t j = s_relayed; j < s_issued; ++j)
-      if (j != s_withheld) mbar_wait_stage(&full_bar[j % STAGES], (j / STAGES) & 1u, &never, p.status, p.wait_ns);
+  if (warp == 0 && lane == 0 && *s_abort) {
+    store_rank(&s_drain, 0, 1);
+    store_rank(&s_drain, 1, 1);
   }
   __syncwarp();
   tc_fence_before();
   asm volatile("bar.sync 0;" ::: "memory");
-  cluster_sync();   // both CTAs are past their last remote arrival and MMA
+  cluster_sync();   // both CTAs are past their last arrival, copy issue and MMA
+  if (warp == 0 && lane == 0 && s_drain) {
+    // After an abort, copies issued but not waited for must land before the
+    // CTAs end. A stage that only one CTA issued gets the other's arrival
+    // here, so that its barrier completes with the copies that there are.
+    const uint32_t own = s_issued, other = load_rank(&s_issued, rank ^ 1u), last = max(own, other);
+    const uint32_t other_tails = load_rank(&s_tails, rank ^ 1u);
+    int never = 0;
+    for (uint32_t j = last > STAGES ? last - STAGES : 0; j < last; ++j) {
+      const uint32_t s = j % STAGES;
+      const bool mine = j < own && j != s_withheld;
+      if (((j < own ? s_tails : other_tails) >> s) & 1u) {
+        if (mine) mbar_wait_stage(&tail_bar[s], (s_tail_phase >> s) & 1u, &never, p.status, p.wait_ns);
+      } else {
+        if (!mine) mbar_arrive_pair(map_rank(&full_bar[s], 0));
+        if (rank == 0) mbar_wait_stage<true>(&full_bar[s], (j / STAGES) & 1u, &never, p.status, p.wait_ns);
+      }
+    }
+  }
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, TMEM_COLS);
   }
+  __syncwarp();
   cluster_sync();
   } else {
     // -------------------------------------------------------------- epilogue
@@ -576,7 +619,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
         const uint32_t buf = tb & 1u;
         // one warp polls, the others sleep in the barrier
         const bool got =
-            q != 0 || mbar_wait_stage(&tfull_bar[buf], (tb >> 1) & 1u, s_abort, p.status, p.wait_ns);
+            q != 0 || mbar_wait_stage<true>(&tfull_bar[buf], (tb >> 1) & 1u, s_abort, p.status, p.wait_ns);
         if (!epilogue_all(wg, got)) return false;
         tc_fence_after();
         tbase = tmem_base + (uint32_t(q * 32) << 16) + buf * TMEM_BUF;
@@ -584,8 +627,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
       };
       auto release = [&]() {   // its values are in registers: hand it back
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_rank(&tempty_bar[tb & 1u], 0);
+        epilogue_sync(wg);
+        if (q == 0 && lane == 0) mbar_arrive_pair(map_rank(&tempty_bar[tb & 1u], 0));
         ++tb;
       };
       uint32_t tbase;
