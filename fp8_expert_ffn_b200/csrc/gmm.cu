@@ -79,15 +79,19 @@ constexpr int TMEM_BUF = 256;           // TMEM columns of one of the two accumu
 // 65 experts, 1 GB of weights, 190 -> 184 us).
 constexpr int stage_bytes(int BR) { return A_BYTES + BR * BK; }   // each CTA holds half of the rows
 
-// PROMOTE: fp32 outputs over a long contraction. The MMA adds to its fp32
-// accumulator by truncation, so a sum's error grows with the number of its
-// additions (2.3e-6 of the result after 2,600 terms, twenty times that of an
-// fp32 product). These tiles hand the accumulator over every SEGMENT K blocks
-// (512 terms) and the epilogue adds the parts in registers, rounding to
-// nearest: 8 warps with 128 rows of a column each, their registers taken from
-// the other warps as in the FP8 GEMMs. 16-bit outputs, whose rounding is a
-// thousand times larger, keep one sum.
-constexpr int SEGMENT = 8;
+// PROMOTE: a contraction too long for one accumulator. The MMA adds to its
+// fp32 accumulator by truncation, so a sum's error grows with its length: for
+// terms of one sign by 0.85 2^-23 of the result per 16 terms (measured to
+// 65,536 fp16 terms, where it was 0.86 of half a step of the output). These
+// tiles hand the accumulator over every segment of K blocks and the epilogue
+// adds the parts in registers, rounding to nearest: 8 warps with 128 rows of a
+// column each, their registers taken from the other warps as in the FP8 GEMMs.
+// The segment follows from the output's type: 512 terms for fp32 (2.3e-6 of
+// the result after 2,600 terms in one sum, 4.7e-7 so), and where the
+// truncation is at most 0.08 of half a step, 6,144 terms for fp16 and
+// 49,152 for bf16. A tile's own length decides where its sum is cut, so its
+// bits do not depend on the rest of the launch.
+constexpr int segment(moe_dtype out) { return out == MOE_F32 ? 8 : out == MOE_F16 ? 96 : 768; }
 
 // Epilogue warps: two warpgroups with 128 rows each, or one where tiles have
 // 64 rows (with one for 256 rows, a weight gradient over 512 rows per group
@@ -115,6 +119,7 @@ struct GmmArgs {
   void* out;
   long long ld;             // output row stride, elements
   int out_type;             // moe_dtype
+  int segment;              // PROMOTE: K blocks of one accumulator
   int accumulate;           // wgrad: add to what `out` holds
   int bulk;                 // the output takes bulk tensor stores (aligned base and stride),
   int bulk_edge;            // also of boxes that reach past its last column: they write whole
@@ -418,9 +423,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
       for (int w = 0, i; ok && (i = tile_at(w, pair, npairs)) < total; ++w) {
         const Tile t = decode_tile<MODE, BR>(i, s_tiles, p);
         if (t.nk == 0) continue;
+        int part = 0;   // K blocks in the accumulator
         const uint32_t idesc = p.idesc | (uint32_t(tile_n(t) >> 3) << 17);
         for (int kb = 0; kb < t.nk; ++kb) {
-          const int part = PROMOTE ? kb % SEGMENT : kb;   // K block within the accumulator's sum
           const uint32_t buf = tb & 1u;
           if (part == 0 &&
               !mbar_wait_stage<true>(&tempty_bar[buf], ((tb >> 1) & 1u) ^ 1u, s_abort, p.status, p.wait_ns)) {
@@ -445,9 +450,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
                          (part | k) ? 1u : 0u);
           tc_commit_pair(&empty_bar[s]);
           ++it;
-          if (kb == t.nk - 1 || (PROMOTE && part == SEGMENT - 1)) {
+          ++part;
+          if (kb == t.nk - 1 || (PROMOTE && part == p.segment)) {
             tc_commit_pair(&tfull_bar[buf]);
             ++tb;
+            part = 0;
           }
         }
       }
@@ -647,9 +654,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc)
 #pragma unroll
-          for (int j = 0; j < 32; ++j) acc[cc][j] = 0.0f;
+          for (int j = 0; j < 32; ++j) acc[cc][j] = -0.0f;   // the first part as it is, -0 too
         bool ok = true;
-        for (int kb = 0; kb < t.nk; kb += SEGMENT) {
+        for (int kb = 0; kb < t.nk; kb += p.segment) {
           if (!accumulator(tbase)) { ok = false; break; }
 #pragma unroll
           for (int cc = 0; cc < 4; ++cc) {
@@ -722,7 +729,7 @@ cudaError_t launch_variant(const moe_layer_s* L, const CUtensorMap& tmA, const R
 template <int MODE, int BR>
 cudaError_t launch_mode(const moe_layer_s* L, const CUtensorMap& tmA, const RowMaps& tmB, const GmmArgs& a, int terms,
                         long long tiles, cudaStream_t st) {
-  if (a.out_type == MOE_F32 && terms > SEGMENT * BK)
+  if (terms > a.segment * BK)
     return launch_variant<MODE, BR, true>(L, tmA, tmB, a, tiles, st);
   return launch_variant<MODE, BR, false>(L, tmA, tmB, a, tiles, st);
 }
@@ -748,6 +755,7 @@ cudaError_t launch_grouped_mm(const moe_layer_s* L, int mode, moe_dtype t, const
   p.out = out;
   p.ld = ldo;
   p.out_type = out_t;
+  p.segment = segment(out_t);
   p.accumulate = accumulate;
   p.status = L->status;
   p.idesc = idesc_16(t, 256, mode != MOE_MM_FORWARD, mode == MOE_MM_WGRAD);

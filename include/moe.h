@@ -422,7 +422,9 @@ moe_status moe_combine(moe_layer_t layer, const uint16_t* y, const int32_t* inv,
  *     that start below 0, decrease or end beyond `rows` set
  *     MOE_STATUS_BAD_PLAN and nothing is written;
  *   - element types are named by moe_dtype; sums are held in fp32 and each
- *     output is rounded once, to nearest even;
+ *     output is rounded once, to nearest even. The 16-bit products' tensor
+ *     core sums truncate, up to 512 terms at a time for fp32 outputs, 6,144
+ *     for fp16 and 49,152 for bf16; these parts are added to nearest;
  *   - NaN and infinities follow IEEE arithmetic and stay in the rows (for
  *     weight gradients: in the groups) that they belong to;
  *   - 1 <= n, k, f <= 65536, row strides at most 2^20 elements, `rows` at

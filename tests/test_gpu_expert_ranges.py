@@ -146,3 +146,84 @@ def test_w4_infinite_last_scale(group, k, zeros, scale_dt):
     want = x[:, :1].float() * k * torch.ones(1, n, device="cuda")
     want[:, ::2] *= float("inf")
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dt", [HF, BF])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("counts", [(1 << 20, 70), (300_001, 0, 200_000)])
+def test_wgrad_of_16_bits_over_many_rows(counts, accumulate, dt):
+    """A weight gradient's contraction is its group's rows. Terms of one sign,
+    so that every truncation of the accumulator goes the same way: the sum may
+    be off by a quarter of half a step of its type before it is rounded."""
+    n, k, G = 72, 136, len(counts)
+    ends = torch.tensor([0, *counts]).cumsum(0)
+    rows = int(ends[-1])
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    draw = lambda c, scale: ((torch.rand(rows, c, generator=gen, device="cuda") + 1) * scale).to(dt)  # noqa: E731
+    x, dy = draw(k, 0.5), draw(n, 2.0 ** -8)
+    L = make_layer(G)
+    offsets = torch.cat([ends, ends[-1:]]).to(torch.int32).cuda()
+    old = torch.randint(0, 100, (G, n, k), generator=gen, device="cuda").to(dt)
+    dw = old.clone()
+    fx.moe_grouped_mm_wgrad(L, CODE[dt], dy, n, x, k, offsets, rows, n, k, CODE[dt], dw, k, accumulate)
+    status_ok(L)
+    half = torch.finfo(dt).eps / 2
+    for g, (a, b) in enumerate(zip(ends[:-1].tolist(), ends[1:].tolist())):
+        want = torch.zeros(n, k, dtype=torch.float64, device="cuda")
+        for i in range(a, b, 1 << 17):
+            want += dy[i:min(b, i + (1 << 17))].double().T @ x[i:min(b, i + (1 << 17))].double()
+        if accumulate:
+            want += old[g].double()
+        err = (dw[g].double() - want).abs()
+        assert (err <= 1.25 * half * want.abs()).all(), (g, (err / (half * want.abs())).max().item())
+
+
+@pytest.mark.parametrize("dt", [HF, BF])
+@pytest.mark.parametrize("op", ["mm", "dgrad"])
+def test_products_of_16_bits_over_the_longest_contraction(op, dt):
+    """65,536 terms of one sign; the bound is the weight gradients'."""
+    counts, long, short = (150, 0, 40), 1 << 16, 264
+    n, k = (short, long) if op == "mm" else (long, short)
+    ends = torch.tensor([0, *counts]).cumsum(0)
+    rows, G = int(ends[-1]), len(counts)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    draw = lambda *s, scale: ((torch.rand(*s, generator=gen, device="cuda") + 1) * scale).to(dt)  # noqa: E731
+    a, w = draw(rows, long, scale=0.5), draw(G, n, k, scale=2.0 ** -8)
+    L = make_layer(G)
+    offsets = torch.cat([ends, ends[-1:]]).to(torch.int32).cuda()
+    y = torch.empty(rows, short, dtype=dt, device="cuda")
+    call = fx.moe_grouped_mm if op == "mm" else fx.moe_grouped_mm_dgrad
+    call(L, CODE[dt], a, long, w, k, offsets, rows, n, k, CODE[dt], y, short)
+    status_ok(L)
+    half = torch.finfo(dt).eps / 2
+    for g, (s, e) in enumerate(zip(ends[:-1].tolist(), ends[1:].tolist())):
+        want = a[s:e].double() @ (w[g].double().T if op == "mm" else w[g].double())
+        assert ((y[s:e].double() - want).abs() <= 1.25 * half * want.abs()).all(), g
+
+
+@pytest.mark.parametrize("dt,out_dt", [(HF, HF), (BF, F32)])
+def test_wgrad_group_does_not_depend_on_the_others(dt, out_dt):
+    """A group's gradient has the same bits in a launch of its own rows and in
+    a longer one: where a sum is cut follows from the group's rows alone."""
+    n, k = 136, 264
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    for counts in ((300, 9000), (3000, 9000), (7001, 513, 20000)):
+        ends = [0]
+        for c in counts:
+            ends.append(ends[-1] + c)
+        x = torch.randn(ends[-1], k, generator=gen, device="cuda").to(dt)
+        dy = (torch.randn(ends[-1], n, generator=gen, device="cuda") * 0.1).to(dt)
+        all_ = torch.empty(len(counts), n, k, dtype=out_dt, device="cuda")
+        L = make_layer(len(counts))
+        off = torch.tensor(ends + ends[-1:], dtype=torch.int32, device="cuda")
+        fx.moe_grouped_mm_wgrad(L, CODE[dt], dy, n, x, k, off, ends[-1], n, k, CODE[out_dt], all_, k)
+        one = make_layer(1)
+        for g, c in enumerate(counts):
+            a, b = ends[g], ends[g + 1]
+            alone = torch.empty(1, n, k, dtype=out_dt, device="cuda")
+            xs, ds = x[a:b].clone(), dy[a:b].clone()
+            fx.moe_grouped_mm_wgrad(one, CODE[dt], ds, n, xs, k, torch.tensor([0, c, c], dtype=torch.int32, device="cuda"),
+                                    c, n, k, CODE[out_dt], alone, k)
+            assert torch.equal(alone[0].view(torch.uint8), all_[g].view(torch.uint8)), (counts, g)
+        status_ok(L)
+        status_ok(one)
