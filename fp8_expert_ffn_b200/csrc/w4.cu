@@ -19,9 +19,10 @@
 // permutes. tcgen05 would need the unpacked weights back in shared or tensor
 // memory, a second trip per code that the memory-bound case has no use for.
 //
-// Layout: 4 warps per CTA, 3 CTAs per SM, persistent over (group, column tile,
-// rows chunk). A warp owns 64 weight rows (32 gate and 32 up) and every wk-th
-// stage of the contraction, and streams its codes through its own ring of two
+// Layout: 4 warps per CTA, 3 CTAs per SM (2 for units of 16 rows), persistent
+// over (group, column tile, rows chunk). A warp owns 64 weight rows (32 gate
+// and 32 up) and every wk-th stage of the contraction, and streams its codes
+// through its own ring of two
 // TMA boxes (64 rows x 128 bytes = 256 codes, 128-byte swizzle: lane (g, t)
 // reads word t of a chunk of row g without bank conflicts), so no warp waits
 // for another until a unit's partial sums meet in shared memory, added in
@@ -48,7 +49,10 @@ namespace {
 
 constexpr int THREADS = 128;
 constexpr int WARPS = THREADS / 32;
-constexpr int CTAS_PER_SM = 3;
+// For units of 8 nt rows. Held to the registers of 3 CTAs, the kernels for 16
+// rows spill 250 to 810 bytes (32 rows in each of 64 groups, gate/up of
+// 1536 x 5120: 585 us against 407).
+constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
 constexpr int KB = 256;                    // codes per row of a stage
 constexpr int KH = KB / 2;                 // and of the half that is worked on at a time
 constexpr int STAGES = 2;
@@ -379,7 +383,7 @@ __device__ __forceinline__ void column_sync(int nw, int wk) {
 }
 
 template <bool BF16, int GS, bool ZEROS, int NT>
-__global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
+__global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
     w4_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1, const W4Args p) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   constexpr int RMAX = 8 * NT;   // rows of a unit
@@ -578,7 +582,7 @@ cudaError_t launch(const moe_layer_s* L, const CUtensorMap& tm0, const CUtensorM
     a.withhold = 1;
     L->test_stall_ns = 0;
   }
-  const long long cap = static_cast<long long>(CTAS_PER_SM) * L->num_sms;
+  const long long cap = static_cast<long long>(ctas_per_sm(NT)) * L->num_sms;
   const dim3 grid(unsigned(units < cap ? units : cap));
   return launch_pdl(w4_kernel<BF16, GS, ZEROS, NT>, grid, dim3(THREADS), SMEM_DYN, st, tm0, tm1, a);
 }
@@ -632,7 +636,12 @@ cudaError_t launch_w4(const moe_layer_s* L, moe_dtype t, const void* x, int x_ro
             reinterpret_cast<uintptr_t>(p.zeros[i]) % gps == 0;
   p.nkb = (k + KB - 1) / KB;
   // Rows of a unit: 8, or 16 when groups hold more than 8 on average (the
-  // codes are then unpacked half as often, on two thirds of the warps).
+  // codes are then unpacked half as often, on two thirds of the warps). With
+  // 64 groups and 8, 10, 16, 24, 32 and 64 rows in each, gate/up of
+  // 1536 x 5120 takes 148, 268, 259, 367, 492 and 963 us by units of 8 and
+  // 208, 219, 229, 412, 407 and 766 by units of 16; with the same means
+  // spread unevenly 178, 211, 319, 419, 536 and 1002 against 213, 218, 288,
+  // 380, 504 and 851.
   const int nt = rows > 8ll * G ? 2 : 1;
   // units per column tile, at most: a group adds at most one that is not full
   long long groups = rows / (8 * nt) + (rows < G ? rows : G);
@@ -645,7 +654,7 @@ cudaError_t launch_w4(const moe_layer_s* L, moe_dtype t, const void* x, int x_ro
   // or one matrix (30.7 us against 34.8 two ways and 53 one way), 2 ways for
   // a decode batch of 64 (422 against 430 one way and 463 four ways) and for
   // the down projection of 16 tokens (78 against 84 and 92).
-  const double ctas = double(CTAS_PER_SM) * L->num_sms;
+  const double ctas = double(ctas_per_sm(nt)) * L->num_sms;
   const double touched = G * (1.0 - exp(-double(rows) / G)) + double(rows) / (16 * nt);
   double best = 0.0;
   for (int wk = WARPS; wk >= 1; wk /= 2) {

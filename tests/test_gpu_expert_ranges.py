@@ -227,3 +227,39 @@ def test_wgrad_group_does_not_depend_on_the_others(dt, out_dt):
             assert torch.equal(alone[0].view(torch.uint8), all_[g].view(torch.uint8)), (counts, g)
         status_ok(L)
         status_ok(one)
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_w4_units_of_16_rows(group, zeros, dt):
+    """More than 8 rows per group on average: integers bit for bit, for every
+    kernel of the wider units, and the gate/up form against its two products."""
+    counts, n, k = (16, 40, 1, 15, 0, 33), 104, 552
+    G, rows, ng, ld = len(counts), sum(counts), -(-k // group), k // 2 // 16 * 16 + 16
+    gen = torch.Generator(device="cuda").manual_seed(group)
+    rand = lambda hi, *s: torch.randint(0, hi, s, generator=gen, device="cuda")  # noqa: E731
+
+    def weights():
+        codes, sc = rand(256, G, n, ld).to(torch.uint8), 2.0 ** (rand(3, G, n, ng) - 1).float()
+        zp = rand(16, G, n, ng).to(torch.uint8) if zeros else None
+        q = torch.stack((codes & 15, codes >> 4), -1).view(G, n, -1)[:, :, :k].double()
+        wide = lambda v: v.double().repeat_interleave(group, -1)[:, :, :k]  # noqa: E731
+        return fx.W4Weights(codes, sc.to(dt), zp, CODE[dt], group), (q - (wide(zp) if zeros else 8.0)) * wide(sc)
+
+    (gate, g64), (up, u64) = weights(), weights()
+    x = (rand(5, rows, k) - 2).to(dt)
+    ends = torch.tensor([0, *counts]).cumsum(0)
+    offsets = torch.cat([ends, ends[-1:]]).to(torch.int32).cuda()
+    L = make_layer(G)
+    y, h = torch.empty(rows, n, device="cuda"), torch.empty(rows, n, device="cuda")
+    fx.moe_w4_matvec(L, CODE[dt], x, rows, k, None, gate, offsets, rows, n, k, fx.MOE_F32, y, n)
+    fx.moe_w4_gate_up(L, CODE[dt], x, rows, k, None, gate, up, offsets, rows, n, k, fx.MOE_F32, h, n)
+    status_ok(L)
+    for g, (a, b) in enumerate(zip(ends[:-1].tolist(), ends[1:].tolist())):
+        gv, uv = x[a:b].double() @ g64[g].T, x[a:b].double() @ u64[g].T
+        assert torch.equal(y[a:b].double(), gv), g      # halves below 2^20: exact in fp32
+        want = gv * torch.sigmoid(gv) * uv
+        # exp within (|gate| + 8) 2^-23, six roundings of 2^-24, as silu's bound above
+        rel = (gv.abs() + 16) * 2.0 ** -23 + 5 * 2.0 ** -149 / torch.exp(gv.clamp(min=-205, max=0) / 2)
+        assert ((h[a:b].double() - want).abs() <= rel * want.abs() + rounding(F32, want)).all(), g
