@@ -28,7 +28,7 @@
 //   warp 0      TMA producer into a ring of 6 stages (16 KB of A, up to 16 KB of B)
 //   warp 1      TMEM allocation; in the leading CTA the MMA issuer
 //   warp 2      wgrad: clears its CTA's half of a tail
-//   warp 3      idle
+//   warp 3      in the other CTA: hands accumulators back to the leading one
 //   warps 4-11  epilogue, two warpgroups with 128 output rows each: TMEM lanes
 //               32*(w%4).., one output column per lane; two 256-column TMEM
 //               buffers overlap it with the next tile. Outputs go through
@@ -45,9 +45,9 @@
 // wrote at cluster scope), where each CTA has announced its own. Only a wgrad
 // tail completes on its CTA's own barrier, and that CTA arrives on the leading
 // one's when the zeros lie. Waits on barriers that the other CTA signals
-// acquire, and arrivals by threads release, at cluster scope. One thread per
-// warpgroup hands an accumulator back: a release by each warp cost the wgrad
-// over 512 rows per group 2 of its 101 us.
+// acquire, and arrivals by threads release, at cluster scope. The other CTA's
+// epilogue leaves the release of an accumulator to warp 3 (a release by its
+// own warps held the wgrad over 512 rows per group up by 7 of 101 us).
 // No TMA multicast; commits signal both CTAs. Every wait is bounded (1 s): on
 // a timeout the status word is set, all roles leave, copies in flight are
 // waited for (bounded) and the TMEM is released.
@@ -287,7 +287,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
   __shared__ __align__(8) uint64_t tail_bar[STAGES];    // wgrad: this CTA's copies of a group's last block
   __shared__ __align__(8) uint64_t empty_bar[STAGES];
   __shared__ __align__(8) uint64_t tfull_bar[2];
-  __shared__ __align__(8) uint64_t tempty_bar[2];       // leading CTA: both CTAs' epilogues
+  __shared__ __align__(8) uint64_t tread_bar[2];        // this CTA's epilogue has read the accumulator
+  __shared__ __align__(8) uint64_t tempty_bar[2];       // leading CTA: the other one's has
   __shared__ __align__(8) uint64_t done_bar;
   __shared__ __align__(8) uint64_t zero_bar;            // wgrad: zeros copied over a tail
   __shared__ TileList s_tiles;
@@ -312,7 +313,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull_bar[b], 1);
-      mbar_init(&tempty_bar[b], 2 * (EPI_WARPS / 4));
+      mbar_init(&tread_bar[b], EPI_WARPS);
+      mbar_init(&tempty_bar[b], 1);
     }
     mbar_init(&done_bar, 1);
     mbar_init(&zero_bar, 1);
@@ -428,7 +430,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
         for (int kb = 0; kb < t.nk; ++kb) {
           const uint32_t buf = tb & 1u;
           if (part == 0 &&
-              !mbar_wait_stage<true>(&tempty_bar[buf], ((tb >> 1) & 1u) ^ 1u, s_abort, p.status, p.wait_ns)) {
+              !(mbar_wait_stage(&tread_bar[buf], ((tb >> 1) & 1u) ^ 1u, s_abort, p.status, p.wait_ns) &&
+                mbar_wait_stage<true>(&tempty_bar[buf], ((tb >> 1) & 1u) ^ 1u, s_abort, p.status, p.wait_ns))) {
             ok = false;
             break;
           }
@@ -499,6 +502,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
       }
       zero_phase ^= 1u;
       if (lane == 0) mbar_arrive_pair(full + s * 8);
+    }
+  } else if (warp == 3 && rank == 1) {
+    // ----------------------------------------------- accumulators handed back
+    if (elect_one()) {
+      const uint32_t tempty = map_rank(tempty_bar, 0);
+      uint32_t tb = 0;
+      bool ok = true;
+      for (int w = 0, i; ok && (i = tile_at(w, pair, npairs)) < total; ++w) {
+        const int nk = decode_tile<MODE, BR>(i, s_tiles, p).nk;
+        for (int kb = 0; ok && kb < nk; kb += PROMOTE ? p.segment : nk) {
+          ok = mbar_wait_stage(&tread_bar[tb & 1u], (tb >> 1) & 1u, s_abort, p.status, p.wait_ns);
+          if (ok) mbar_arrive_pair(tempty + (tb & 1u) * 8);
+          ++tb;
+        }
+      }
     }
   }
   // ------------------------------------------------ teardown (warps 0 to 3)
@@ -634,8 +652,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
       };
       auto release = [&]() {   // its values are in registers: hand it back
         tc_fence_before();
-        epilogue_sync(wg);
-        if (q == 0 && lane == 0) mbar_arrive_pair(map_rank(&tempty_bar[tb & 1u], 0));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tread_bar[tb & 1u]);
         ++tb;
       };
       uint32_t tbase;
