@@ -84,6 +84,30 @@ def test_swiglu_low_gates_and_large_factors(dt, pad):
     assert torch.equal(h.view(torch.uint8)[:, :f], h2.view(torch.uint8)[:, :f])
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_swiglu_low_gates_in_place(dt):
+    """Rows whose elements are computed one by one, outputs over the inputs."""
+    rows, f = 9, 72
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    g, u, d = (torch.randn(rows, f, generator=gen, device="cuda") * 2 for _ in range(3))
+    g[::2, 5] = -88.0
+    u[::2, 5] = 1e38
+    u[1, 7], d[1, 7] = 3e38, 1e5
+    g, u, d = g.to(dt), u.to(dt), d.to(dt)
+    L, t = make_layer(1), CODE[dt]
+    h, dg, du = torch.empty_like(g), torch.empty_like(g), torch.empty_like(g)
+    fx.moe_swiglu(L, t, g, f, u, f, None, rows, f, h, f)
+    fx.moe_swiglu_backward(L, t, d, f, g, f, u, f, None, rows, f, dg, f, du, f)
+    gi, ui, di = g.clone(), u.clone(), d.clone()
+    fx.moe_swiglu_backward(L, t, di, f, gi, f, ui, f, None, rows, f, gi, f, ui, f, di, f)
+    assert torch.equal(gi, dg) and torch.equal(ui, du) and torch.equal(di, h)
+    for target in (0, 1):
+        gi, ui = g.clone(), u.clone()
+        fx.moe_swiglu(L, t, gi, f, ui, f, None, rows, f, (gi, ui)[target], f)
+        assert torch.equal((gi, ui)[target], h)
+    status_ok(L)
+
+
 @pytest.mark.parametrize("dt,out_dt", [(BF, BF), (HF, F32), (BF, F32)])
 def test_w4_gate_up_low_gates(dt, out_dt):
     """The gate/up form's activation where exp(-gate) is beyond fp32: one
