@@ -16,9 +16,11 @@
 // The operands are read as they lie in memory: forward, both K-major; dgrad,
 // A = w with the contraction n as its slow dimension (MN-major); wgrad, both
 // MN-major over the group's rows. A wgrad block that passes the group's end
-// has zeros copied over the rows past it in shared memory before the MMA (in
-// both operands, so that a NaN there is not multiplied by zero; by bulk
-// copies: with plain stores a tile with a tail waited 4 thousand cycles).
+// (a tail) must not see the rows past it, in either operand: a NaN there would
+// not vanish by a zero in the other one. It is loaded by boxes of 32, 8, 2 and
+// 1 rows that end with the group, the MMA takes only as many 16-row slices as
+// hold its rows, and what is left of the last slice comes from boxes past the
+// operand's last row, which the copies fill with zeros.
 //
 // Kernel layout: CTA pairs (cluster of 2, tcgen05 cta_group::2, M 256 x N up
 // to 256 x K 16 per instruction), persistent over a device-side tile list.
@@ -27,8 +29,8 @@
 // independent 128 x 256 tiles would move 48 KB.
 //   warp 0      TMA producer into a ring of 6 stages (16 KB of A, up to 16 KB of B)
 //   warp 1      TMEM allocation; in the leading CTA the MMA issuer
-//   warp 2      wgrad: clears its CTA's half of a tail
-//   warp 3      in the other CTA: hands accumulators back to the leading one
+//   warp 2      in the other CTA: hands accumulators back to the leading one
+//   warp 3      idle
 //   warps 4-11  epilogue, two warpgroups with 128 output rows each: TMEM lanes
 //               32*(w%4).., one output column per lane; two 256-column TMEM
 //               buffers overlap it with the next tile. Outputs go through
@@ -42,17 +44,18 @@
 // Hand-over between the CTAs: the leading CTA's MMA reads stages that lie in
 // the other one, so both CTAs' copies complete on the leading CTA's barrier
 // (the cta_group::2 form of the loads; a completion releases what its copy
-// wrote at cluster scope), where each CTA has announced its own. Only a wgrad
-// tail completes on its CTA's own barrier, and that CTA arrives on the leading
-// one's when the zeros lie. Waits on barriers that the other CTA signals
-// acquire, and arrivals by threads release, at cluster scope. The other CTA's
-// epilogue leaves the release of an accumulator to warp 3 (a release by its
-// own warps held the wgrad over 512 rows per group up by 7 of 101 us).
+// wrote at cluster scope), where each CTA has announced its own. Waits on
+// barriers that the other CTA signals acquire, and arrivals by threads release,
+// at cluster scope. The other CTA's epilogue leaves the release of an
+// accumulator to warp 2 (a release by its own warps held the wgrad over 512
+// rows per group up by 7 of 101 us).
 // No TMA multicast; commits signal both CTAs. Every wait is bounded (1 s): on
 // a timeout the status word is set, all roles leave, copies in flight are
 // waited for (bounded) and the TMEM is released.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "groups.cuh"
@@ -99,11 +102,8 @@ constexpr int segment(moe_dtype out) { return out == MOE_F32 ? 8 : out == MOE_F1
 constexpr int epi_warps(int BR, bool promote) { return BR == 256 || promote ? 8 : 4; }
 constexpr int threads(int BR, bool promote) { return 32 * (FIRST_EPI_WARP + epi_warps(BR, promote)); }
 constexpr int stages(int BR, bool promote) { return BR == 256 ? 6 : 10; }
-// Two staged chunks: one per warpgroup, or two of the only one; wgrad's zeros
-// (one box) lie behind them.
-constexpr int smem_dyn(int mode, int BR, bool promote) {
-  return stages(BR, promote) * stage_bytes(BR) + 2 * STG_BYTES + (mode == MOE_MM_WGRAD ? BOX_BYTES : 0) + 1024;
-}
+// Two staged chunks: one per warpgroup, or two of the only one.
+constexpr int smem_dyn(int BR, bool promote) { return stages(BR, promote) * stage_bytes(BR) + 2 * STG_BYTES + 1024; }
 constexpr int LAUNCH_REGS = 168;     // 384 threads, one CTA per SM
 constexpr int PRODUCER_REGS = 40;
 constexpr int EPILOGUE_REGS = 232;
@@ -135,11 +135,21 @@ struct GmmArgs {
 struct RowMaps {
   CUtensorMap m[4];
 };
+// wgrad: dy by boxes of 64 rows, and the boxes of a tail (32, 8, 2 and 1 rows)
+// of x and dy.
+struct WgradMaps {
+  CUtensorMap m;
+  CUtensorMap a[4], b[4];
+};
+constexpr int tail_rows(int i) { return i == 0 ? 32 : i == 1 ? 8 : i == 2 ? 2 : 1; }
+template <int MODE>
+using BMaps = typename std::conditional<MODE == MOE_MM_WGRAD, WgradMaps, RowMaps>::type;
 
 struct Tile {
-  int g, col0, row0, nrows, r_first, nk;
+  int g, col0, row0, nrows, r_first, terms, nk;
   // row0: first output row (global for forward/dgrad, within the group's
-  // weight for wgrad); nrows: valid rows; r_first, wgrad: the group's first row
+  // weight for wgrad); nrows: valid rows; wgrad: the group's first row and its
+  // rows; nk: K blocks
 };
 
 // The tile list. Forward and dgrad keep the groups' order: a group's weights
@@ -193,11 +203,11 @@ __device__ __forceinline__ Tile decode_tile(int i, const TileList& s, const GmmA
     t.row0 = (ct % rts) * BR;
     t.nrows = min(BR, p.nr - t.row0);
     t.r_first = s.plan.off[t.g];
-    const int n_g = s.plan.off[t.g + 1] - t.r_first;
-    t.nk = (n_g + BK - 1) / BK;
+    t.terms = s.plan.off[t.g + 1] - t.r_first;
+    t.nk = (t.terms + BK - 1) / BK;
     return t;
   }
-  t.r_first = 0;
+  t.r_first = t.terms = 0;
   t.nk = p.nk;
   // chunks of up to 8 row tiles, then the column tiles, then the row tiles:
   // the row tiles that share a weight tile run side by side
@@ -276,7 +286,7 @@ __device__ __forceinline__ bool epilogue_all(int wg, bool ok) {
 
 template <int MODE, int BR, bool PROMOTE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE), 1)
-    grouped_mm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ RowMaps tmB,
+    grouped_mm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMaps<MODE> tmB,
                       const __grid_constant__ CUtensorMap tmO, const GmmArgs p) {
   constexpr bool A_MN = MODE != MOE_MM_FORWARD;   // A's contraction is its slow dimension
   constexpr bool B_MN = MODE == MOE_MM_WGRAD;
@@ -284,20 +294,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
   constexpr int THREADS = threads(BR, PROMOTE), EPI_WARPS = epi_warps(BR, PROMOTE);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[STAGES];    // leading CTA: both CTAs' parts of a stage
-  __shared__ __align__(8) uint64_t tail_bar[STAGES];    // wgrad: this CTA's copies of a group's last block
   __shared__ __align__(8) uint64_t empty_bar[STAGES];
   __shared__ __align__(8) uint64_t tfull_bar[2];
   __shared__ __align__(8) uint64_t tread_bar[2];        // this CTA's epilogue has read the accumulator
   __shared__ __align__(8) uint64_t tempty_bar[2];       // leading CTA: the other one's has
   __shared__ __align__(8) uint64_t done_bar;
-  __shared__ __align__(8) uint64_t zero_bar;            // wgrad: zeros copied over a tail
   __shared__ TileList s_tiles;
   __shared__ uint32_t tmem_base_s;
   __shared__ int s_abort_store;
   __shared__ uint32_t s_issued, s_withheld, s_drain;
-  __shared__ uint32_t s_tails, s_tail_phase;   // a bit per slot: its last stage was a tail; parity of its last tail
-  __shared__ uint32_t s_progress_store;        // stages issued so far, by tiles
-  volatile uint32_t* s_progress = &s_progress_store;
   volatile int* s_abort = &s_abort_store;
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -308,7 +313,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full_bar[s], 2);
-      mbar_init(&tail_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -317,20 +321,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
       mbar_init(&tempty_bar[b], 1);
     }
     mbar_init(&done_bar, 1);
-    mbar_init(&zero_bar, 1);
     s_abort_store = 0;
     s_issued = 0;
     s_drain = 0;
-    s_tails = 0;
-    s_tail_phase = 0;
-    s_progress_store = 0;
     s_withheld = 0xFFFFFFFFu;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmA);
-    for (int j = 0; j < (B_MN ? 1 : 4); ++j) tma_prefetch_desc(&tmB.m[j]);
+    if constexpr (B_MN)
+      tma_prefetch_desc(&tmB.m);
+    else
+      for (int j = 0; j < 4; ++j) tma_prefetch_desc(&tmB.m[j]);
   }
   if (warp == 1) tmem_alloc_pair(&tmem_base_s, TMEM_COLS);
   // the set-up above overlaps the previous kernel; offsets, operands and
@@ -352,47 +355,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
     // -------------------------------------------------------------- producer
     if (elect_one()) {
       const uint32_t full = map_rank(full_bar, 0);
-      uint32_t it = 0, tails = 0, tail_next = 0;
+      uint32_t it = 0;
       bool ok = true;
       for (int w = 0, i; ok && (i = tile_at(w, pair, npairs)) < total; ++w) {
         const Tile t = decode_tile<MODE, BR>(i, s_tiles, p);
         const int half = tile_n(t) >> 1;
         const int acol = t.col0 + int(rank) * 128;
         const int brow = t.row0 + int(rank) * half;
-        const uint32_t bytes = A_BYTES + (B_MN ? ((half + 63) >> 6) * BOX_BYTES : half * BK * 2);
-        const bool ragged = MODE == MOE_MM_WGRAD && (s_tiles.plan.off[t.g + 1] - t.r_first) % BK != 0;
+        const int boxes = 2 + (half > 64 ? 2 : 1);   // wgrad: of 64 columns, A's and B's
         for (int kb = 0; kb < t.nk; ++kb) {
           const int s = it % STAGES;
           if (!mbar_wait_stage<true>(&empty_bar[s], ((it / STAGES) & 1u) ^ 1u, s_abort, p.status, p.wait_ns)) {
             ok = false;
             break;
           }
-          // the stage's copies complete on the leading CTA's barrier, or,
-          // where zeros have to follow them, on this CTA's own
-          const bool tail = ragged && kb == t.nk - 1;
-          if (MODE == MOE_MM_WGRAD) tails = tail ? tails | (1u << s) : tails & ~(1u << s);
           if (p.withhold && blockIdx.x == 0 && it == 0) {   // test only: this stage never arrives
             s_withheld = it++;
             continue;
           }
           uint8_t* a = smem + s * STAGE_BYTES;
-          uint8_t* b = a + A_BYTES;
-          const int k0 = (MODE == MOE_MM_WGRAD ? t.r_first : 0) + kb * BK;
           const uint32_t fb = full + s * 8;
-          if (MODE == MOE_MM_WGRAD) {
-            uint32_t bar = fb;
-            if (tail) {
-              bar = smem_u32(&tail_bar[s]);
-              mbar_arrive_expect_tx(&tail_bar[s], bytes);
-              tail_next ^= 1u << s;
+          if constexpr (MODE == MOE_MM_WGRAD) {
+            const int k0 = t.r_first + kb * BK;
+            const int valid = min(BK, t.terms - kb * BK), taken = (valid + 15) & ~15;
+            mbar_expect_pair(fb, uint32_t(boxes * taken) * 128u);
+            if (valid == BK) {
+              tma_load_2d_pair(a, &tmA, fb, acol, k0);
+              tma_load_2d_pair(a + BOX_BYTES, &tmA, fb, acol + 64, k0);
+              tma_load_2d_pair(a + A_BYTES, &tmB.m, fb, brow, k0);
+              if (half > 64) tma_load_2d_pair(a + A_BYTES + BOX_BYTES, &tmB.m, fb, brow + 64, k0);
             } else {
-              mbar_expect_pair(fb, bytes);
+              // A tail. The copies' swizzle goes by the shared-memory address,
+              // so a box may start at any row of a 1024-byte atom. Each issue
+              // names its map (from a map chosen at run time a copy took 170
+              // cycles to issue: 1,151 rows per group 619 us against 454).
+              int r = 0;
+              auto rows_by = [&](const CUtensorMap* ma, const CUtensorMap* mb, int h, int end, int y) {
+                for (; end - r >= h; r += h, y += h) {
+                  uint8_t* dst = a + r * 128;
+                  tma_load_2d_pair(dst, ma, fb, acol, y);
+                  tma_load_2d_pair(dst + BOX_BYTES, ma, fb, acol + 64, y);
+                  tma_load_2d_pair(dst + A_BYTES, mb, fb, brow, y);
+                  if (half > 64) tma_load_2d_pair(dst + A_BYTES + BOX_BYTES, mb, fb, brow + 64, y);
+                }
+              };
+#pragma unroll
+              for (int j = 0; j < 4; ++j) rows_by(&tmB.a[j], &tmB.b[j], tail_rows(j), valid, k0 + r);
+#pragma unroll
+              for (int j = 1; j < 4; ++j) rows_by(&tmB.a[j], &tmB.b[j], tail_rows(j), taken, p.rows);
             }
-            tma_load_2d_pair(a, &tmA, bar, acol, k0);
-            tma_load_2d_pair(a + BOX_BYTES, &tmA, bar, acol + 64, k0);
-            for (int c = 0; c < half; c += 64) tma_load_2d_pair(b + c * (BK * 2), &tmB.m[0], bar, brow + c, k0);
           } else {
-            mbar_expect_pair(fb, bytes);
+            uint8_t* b = a + A_BYTES;
+            const int k0 = kb * BK;
+            mbar_expect_pair(fb, A_BYTES + half * BK * 2);
             if (MODE == MOE_MM_FORWARD) {
               tma_load_3d_pair(a, &tmA, fb, k0, acol, t.g);
             } else {
@@ -411,11 +426,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
           }
           ++it;
         }
-        if (MODE == MOE_MM_WGRAD) *s_progress = it;
       }
       s_issued = it;
-      s_tails = tails;
-      s_tail_phase = ~tail_next;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -445,11 +457,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
           const uint32_t a_addr = smem_u32(smem + s * STAGE_BYTES);
           const uint64_t ad = A_MN ? smem_desc_mn_sw128(a_addr, BOX_BYTES) : smem_desc_sw128(a_addr);
           const uint64_t bd = B_MN ? smem_desc_mn_sw128(a_addr + A_BYTES, BOX_BYTES) : smem_desc_sw128(a_addr + A_BYTES);
+          const int left = MODE == MOE_MM_WGRAD ? t.terms - kb * BK : BK;
 #pragma unroll
           for (int k = 0; k < BK / 16; ++k)
             // 16 of the contraction: 32 bytes along a K-major row, two 8-row
             // atoms (2048 bytes) of an MN-major box (address field in 16 bytes)
-            mma_f16_pair(d, ad + uint64_t(k * (A_MN ? 128 : 2)), bd + uint64_t(k * (B_MN ? 128 : 2)), idesc,
+            if (MODE != MOE_MM_WGRAD || k * 16 < left)
+              mma_f16_pair(d, ad + uint64_t(k * (A_MN ? 128 : 2)), bd + uint64_t(k * (B_MN ? 128 : 2)), idesc,
                          (part | k) ? 1u : 0u);
           tc_commit_pair(&empty_bar[s]);
           ++it;
@@ -465,45 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
       int never = 0;
       mbar_wait_stage(&done_bar, 0, &never, p.status, p.wait_ns);
     }
-  } else if (MODE == MOE_MM_WGRAD && warp == 2) {
-    // ----------------------------------------------------------------- tails
-    uint8_t* zeros = smem + STAGES * STAGE_BYTES + 2 * STG_BYTES;
-    for (int v = lane; v < BOX_BYTES / 16; v += 32) reinterpret_cast<uint4*>(zeros)[v] = make_uint4(0u, 0u, 0u, 0u);
-    fence_proxy_async_smem();
-    __syncwarp();
-    const uint32_t full = map_rank(full_bar, 0);
-    uint32_t it = 0, phase = 0, zero_phase = 0;
-    for (int w = 0, i; (i = tile_at(w, pair, npairs)) < total; ++w) {
-      const Tile t = decode_tile<MODE, BR>(i, s_tiles, p);
-      it += t.nk;
-      const int left = (s_tiles.plan.off[t.g + 1] - t.r_first) % BK;   // the last block's rows, if not all are
-      if (left == 0) continue;
-      const int s = (it - 1) % STAGES;
-      // many tiles may pass before this one: the limit counts from the last stage issued
-      const bool got =
-          mbar_wait_stage(&tail_bar[s], (phase >> s) & 1u, s_abort, p.status, p.wait_ns, s_progress);
-      if (!__all_sync(0xFFFFFFFFu, got)) break;
-      phase ^= 1u << s;
-      // rows [left, 64) of every box belong to the next group (or lie past
-      // the last row): zeros are copied over them
-      if (elect_one()) {
-        const int boxes = 2 + ((tile_n(t) / 2 + 63) >> 6);
-        const uint32_t bytes = uint32_t(BK - left) * 128u;
-        mbar_arrive_expect_tx(&zero_bar, boxes * bytes);
-        for (int bx = 0; bx < boxes; ++bx)
-          bulk_copy_smem(smem + s * STAGE_BYTES + bx * BOX_BYTES + left * 128, zeros, bytes, &zero_bar);
-      }
-      __syncwarp();
-      const bool clean = mbar_wait_stage(&zero_bar, zero_phase, s_abort, p.status, p.wait_ns);
-      if (!__all_sync(0xFFFFFFFFu, clean)) {
-        int never = 0;   // the copies must land before the CTA ends
-        mbar_wait_stage(&zero_bar, zero_phase, &never, p.status, p.wait_ns);
-        break;
-      }
-      zero_phase ^= 1u;
-      if (lane == 0) mbar_arrive_pair(full + s * 8);
-    }
-  } else if (warp == 3 && rank == 1) {
+  } else if (warp == 2 && rank == 1) {
     // ----------------------------------------------- accumulators handed back
     if (elect_one()) {
       const uint32_t tempty = map_rank(tempty_bar, 0);
@@ -535,17 +511,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
     // CTAs end. A stage that only one CTA issued gets the other's arrival
     // here, so that its barrier completes with the copies that there are.
     const uint32_t own = s_issued, other = load_rank(&s_issued, rank ^ 1u), last = max(own, other);
-    const uint32_t other_tails = load_rank(&s_tails, rank ^ 1u);
     int never = 0;
     for (uint32_t j = last > STAGES ? last - STAGES : 0; j < last; ++j) {
       const uint32_t s = j % STAGES;
-      const bool mine = j < own && j != s_withheld;
-      if (((j < own ? s_tails : other_tails) >> s) & 1u) {
-        if (mine) mbar_wait_stage(&tail_bar[s], (s_tail_phase >> s) & 1u, &never, p.status, p.wait_ns);
-      } else {
-        if (!mine) mbar_arrive_pair(map_rank(&full_bar[s], 0));
-        if (rank == 0) mbar_wait_stage<true>(&full_bar[s], (j / STAGES) & 1u, &never, p.status, p.wait_ns);
-      }
+      if (j >= own || j == s_withheld) mbar_arrive_pair(map_rank(&full_bar[s], 0));
+      if (rank == 0) mbar_wait_stage<true>(&full_bar[s], (j / STAGES) & 1u, &never, p.status, p.wait_ns);
     }
   }
   if (warp == 1) {
@@ -706,7 +676,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
 }
 
 template <int MODE, int BR, bool PROMOTE>
-cudaError_t launch_variant(const moe_layer_s* L, const CUtensorMap& tmA, const RowMaps& tmB, GmmArgs a, long long tiles,
+cudaError_t launch_variant(const moe_layer_s* L, const CUtensorMap& tmA, const BMaps<MODE>& tmB, GmmArgs a, long long tiles,
                         cudaStream_t st) {
   // bulk stores want the base and the row stride in 16-byte units; 16-bit
   // accumulation rounds once, which a bulk add to the 16-bit values would not
@@ -728,7 +698,7 @@ cudaError_t launch_variant(const moe_layer_s* L, const CUtensorMap& tmA, const R
     if (PROMOTE && fa.numRegs * threads(BR, PROMOTE) < 128 * PRODUCER_REGS + 256 * EPILOGUE_REGS)
       return cudaErrorInvalidConfiguration;
     return cudaFuncSetAttribute(grouped_mm_kernel<MODE, BR, PROMOTE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                smem_dyn(MODE, BR, PROMOTE));
+                                smem_dyn(BR, PROMOTE));
   });
   if (ce != cudaSuccess) return ce;
   a.wait_ns = kWaitLimitNs;
@@ -740,12 +710,12 @@ cudaError_t launch_variant(const moe_layer_s* L, const CUtensorMap& tmA, const R
   const long long pairs = tiles < L->num_sms / 2 ? tiles : L->num_sms / 2;
   if (pairs <= 0) return cudaSuccess;
   return launch_pdl(grouped_mm_kernel<MODE, BR, PROMOTE>, dim3(unsigned(2 * pairs)), dim3(threads(BR, PROMOTE)),
-                    smem_dyn(MODE, BR, PROMOTE), st, tmA, tmB, tmO, a);
+                    smem_dyn(BR, PROMOTE), st, tmA, tmB, tmO, a);
 }
 
 // `terms`: the longest contraction that the launch may hold.
 template <int MODE, int BR>
-cudaError_t launch_mode(const moe_layer_s* L, const CUtensorMap& tmA, const RowMaps& tmB, const GmmArgs& a, int terms,
+cudaError_t launch_mode(const moe_layer_s* L, const CUtensorMap& tmA, const BMaps<MODE>& tmB, const GmmArgs& a, int terms,
                         long long tiles, cudaStream_t st) {
   if (terms > a.segment * BK)
     return launch_variant<MODE, BR, true>(L, tmA, tmB, a, tiles, st);
@@ -778,19 +748,23 @@ cudaError_t launch_grouped_mm(const moe_layer_s* L, int mode, moe_dtype t, const
   p.status = L->status;
   p.idesc = idesc_16(t, 256, mode != MOE_MM_FORWARD, mode == MOE_MM_WGRAD);
   CUtensorMap tmA;
-  RowMaps tmB;
   if (mode == MOE_MM_WGRAD) {
     // a = dy [rows][n], b = x [rows][k]; output rows n, columns k
     p.nr = n;
     p.nc = k;
     p.ntc = (k + BC - 1) / BC;
-    if (!encode_tmap_16(&tmA, t, b, k, rows, 0, ldb, 64, 64) || !encode_tmap_16(&tmB.m[0], t, a, n, rows, 0, lda, 64, 64))
+    WgradMaps tmB;
+    if (!encode_tmap_16(&tmA, t, b, k, rows, 0, ldb, 64, 64) || !encode_tmap_16(&tmB.m, t, a, n, rows, 0, lda, 64, 64))
       return cudaErrorInvalidValue;
-    for (int j = 1; j < 4; ++j) tmB.m[j] = tmB.m[0];
+    for (int j = 0; j < 4; ++j)
+      if (!encode_tmap_16(&tmB.a[j], t, b, k, rows, 0, ldb, 64, tail_rows(j)) ||
+          !encode_tmap_16(&tmB.b[j], t, a, n, rows, 0, lda, 64, tail_rows(j)))
+        return cudaErrorInvalidValue;
     return launch_mode<MOE_MM_WGRAD, 256>(L, tmA, tmB, p, rows,
                                            static_cast<long long>(G) * ((n + 255) / 256) * p.ntc, st);
   }
   // a = the rows, b = w [G][n][k]
+  RowMaps tmB;
   const int contraction = mode == MOE_MM_FORWARD ? k : n;
   p.nc = mode == MOE_MM_FORWARD ? n : k;
   p.ntc = (p.nc + BC - 1) / BC;

@@ -25,24 +25,19 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar_addr, uint32_
 
 // mbar_wait for the expert operators' stages: looks at the abort flag and the
 // clock only every 32nd poll. Same limit, abort flag and status. CLUSTER: the
-// barrier's arrivals come from both CTAs of a pair. With `progress` the limit
-// starts again whenever what it points to has changed.
+// barrier's arrivals come from both CTAs of a pair.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_stage(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status,
-                                                unsigned long long limit_ns,
-                                                const volatile uint32_t* progress = nullptr) {
+                                                unsigned long long limit_ns) {
   const uint32_t a = smem_u32(bar);
   unsigned long long t0 = 0;
-  uint32_t seen = 0;
   for (uint32_t i = 1;; ++i) {
     if (CLUSTER ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity)) return true;
     if ((i & 31u) == 0) {
       if (*abort) return false;
       const unsigned long long now = globaltimer_ns();
-      const uint32_t at = progress ? *progress : 0;
-      if (t0 == 0 || at != seen) {
+      if (t0 == 0) {
         t0 = now;
-        seen = at;
       } else if (now - t0 > limit_ns) {
         set_status(status, STATUS_WAIT_TIMEOUT);
         *abort = 1;

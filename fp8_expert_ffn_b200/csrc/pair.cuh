@@ -79,14 +79,6 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const void* tmap, ui
       : "memory");
 }
 
-// Bulk copy within this CTA's shared memory (16-byte units), arriving on `bar`.
-__device__ __forceinline__ void bulk_copy_smem(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "r"(smem_u32(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 // Tiled bulk store of one box, and its form that adds (fp32) to memory.
 __device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src, int x, int y, int z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"

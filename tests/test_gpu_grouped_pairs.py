@@ -1,6 +1,6 @@
 """The grouped products' hand-over between the two CTAs of a pair: many short
 tiles, each a few K blocks from operands to output, so that every stage's
-copies, a weight gradient's cleared tails and the accumulators change hands
+copies, a weight gradient's tails and the accumulators change hands
 thousands of times; and waits that give up at each of these points.
 
 Integer inputs: every sum is exact in fp32, so one stale or early operand
