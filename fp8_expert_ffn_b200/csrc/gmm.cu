@@ -37,10 +37,11 @@
 //               shared memory to bulk tensor stores (16-byte aligned rows), or
 //               straight to memory where they cannot.
 // Bound: the tensor cores, at the power limit, for more than about 250 rows
-// per group (a training batch of 36,864 rows over 33 uneven experts,
-// 1536 x 5120: 400 us, 1.45 PFLOP/s; one group of as many rows 354 us where
-// cuBLAS takes 342), HBM below (one decode step of 65 experts: 184 us,
-// 5.6 TB/s).
+// per group. A training batch of 36,864 rows over 33 uneven experts,
+// 1536 x 5120: 508 us back to back (1.14 PFLOP/s; 993 W, SM clock 1177 of 1965
+// MHz) and 402 us one at a time; one group of as many rows 458 and 358 us
+// where cuBLAS takes 437 and 352. HBM below (one decode step of 65 experts:
+// 170 us, 6.1 TB/s).
 // Hand-over between the CTAs: the leading CTA's MMA reads stages that lie in
 // the other one, so both CTAs' copies complete on the leading CTA's barrier
 // (the cta_group::2 form of the loads; a completion releases what its copy
@@ -79,7 +80,7 @@ constexpr int TMEM_BUF = 256;           // TMEM columns of one of the two accumu
 // BR: output rows per tile, at most. 256 fill the MMA; 64 are for a few rows
 // per group, where the stages hold little but weights and more of them can be
 // on their way (10 stages of 20 KB instead of 6 of 32 KB: one decode step of
-// 65 experts, 1 GB of weights, 190 -> 184 us).
+// 65 experts, 1 GB of weights, 178 -> 170 us).
 constexpr int stage_bytes(int BR) { return A_BYTES + BR * BK; }   // each CTA holds half of the rows
 
 // PROMOTE: a contraction too long for one accumulator. The MMA adds to its
@@ -772,7 +773,11 @@ cudaError_t launch_grouped_mm(const moe_layer_s* L, int mode, moe_dtype t, const
   if (!encode_tmap_16(&tmA, t, b, k, n, G, ldb, 64, mode == MOE_MM_FORWARD ? 128 : 64) ||
       !encode_row_maps(&tmB, t, a, contraction, rows, lda))
     return cudaErrorInvalidValue;
-  // few rows per group on average: narrow tiles (larger groups take several)
+  // Few rows per group on average: narrow tiles (larger groups take several).
+  // 64 groups of 1536 x 5120 with 8, 32, 64 and 128 rows in each take 175,
+  // 179, 185 and 235 us by tiles of 64 rows and 184, 187, 189 and 201 by tiles
+  // of 256; by a Zipf law over the groups 172, 188, 227 and 293 against 182,
+  // 182, 185 and 215.
   const int br = rows <= 32ll * G ? 64 : 256;
   // upper bound on the tiles: every group may add one partial row tile
   const long long tiles = (static_cast<long long>(rows) / br + (rows < G ? rows : G)) * p.ntc;

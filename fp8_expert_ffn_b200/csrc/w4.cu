@@ -4,14 +4,16 @@
 // (or 16, see launch_w4) rows, half a byte each, so HBM would bound the kernel
 // if unpacking kept up: 6.5 TB/s is 46 codes per SM and cycle, or 45 issue
 // slots per scheduler for 512 codes, and the kernel takes 38 instructions for
-// them. It runs at 4.35 TB/s (a decode batch of 64 tokens over 257 experts,
-// 1.84 GB: 422 us; without the arithmetic the same copies take 311 us): three
-// warps per scheduler issue 0.55 instructions per cycle.
+// them. It runs at 4.0 TB/s (a decode batch of 64 tokens over 257 experts,
+// 1.84 GB: 450 to 460 us back to back, 433 one at a time, where the same copies
+// without the arithmetic took 311): three warps per scheduler issue 0.55
+// instructions per cycle.
 //
-// Unpacking is exact and short: code nibbles i and i + 4 of a 32-bit word are
-// masked out together and OR-ed into the mantissas of the 16-bit pair
-// (128, 128) in bf16 or (1024, 1024) in fp16; subtracting (128 + z) or
-// (1024 + z) leaves q - z exactly. The pairs go to mma.sync m16n8k16 (weights
+// Unpacking is exact and short (the mantissa trick of Kim, Henry, Fahim and
+// Awadalla, "Who Says Elephants Can't Run", 2022): code nibbles i and i + 4 of
+// a 32-bit word are masked out together and OR-ed into the mantissas of the
+// 16-bit pair (128, 128) in bf16 or (1024, 1024) in fp16; subtracting (128 + z)
+// or (1024 + z) leaves q - z exactly. The pairs go to mma.sync m16n8k16 (weights
 // as A, up to 8 rows of x as one B) with fp32 sums per scale group; the scale
 // multiplies that sum in fp32, so nothing is rounded between the codes and the
 // output. The order of the contraction inside a word (0,4,1,5,...) is the
@@ -22,11 +24,10 @@
 // Layout: 4 warps per CTA, 3 CTAs per SM (2 for units of 16 rows), persistent
 // over (group, column tile, rows chunk). A warp owns 64 weight rows (32 gate
 // and 32 up) and every wk-th stage of the contraction, and streams its codes
-// through its own ring of two
-// TMA boxes (64 rows x 128 bytes = 256 codes, 128-byte swizzle: lane (g, t)
-// reads word t of a chunk of row g without bank conflicts), so no warp waits
-// for another until a unit's partial sums meet in shared memory, added in
-// warp order. The warps of a CTA split the contraction 4, 2 or 1 ways and the
+// through its own ring of two TMA boxes (64 rows x 128 bytes = 256 codes,
+// 128-byte swizzle: lane (g, t) reads word t of a chunk of row g without bank
+// conflicts), so no warp waits for another until a unit's partial sums meet in
+// shared memory, added in warp order. The warps of a CTA split the contraction 4, 2 or 1 ways and the
 // columns by the rest (see launch_w4). Measured and dropped: 16 warps per SM
 // with 128-code stages (465 against 418 us) and 128 rows per warp (500 against
 // 439), both for their 64-byte boxes; 24 warps of 80 registers (no gain at 64
@@ -651,9 +652,10 @@ cudaError_t launch_w4(const moe_layer_s* L, moe_dtype t, const void* x, int x_ro
   // per unit to pay for its fixed cost (finding it, joining the partial sums:
   // 0.4 of a stage's time). The split with the least expected time of a CTA,
   // from the groups that evenly spread rows would touch: 4 ways for one token
-  // or one matrix (30.7 us against 34.8 two ways and 53 one way), 2 ways for
-  // a decode batch of 64 (422 against 430 one way and 463 four ways) and for
-  // the down projection of 16 tokens (78 against 84 and 92).
+  // (24.4 us against 31 two ways and 47 one way) or one matrix (20.2 against
+  // 30.3 and 54), 2 ways for a decode batch of 64 (456 to 465 against 462 to
+  // 471 one way and 480 four ways) and for the down projection of 16 tokens
+  // (77 against 87 and 91 to 98).
   const double ctas = double(ctas_per_sm(nt)) * L->num_sms;
   const double touched = G * (1.0 - exp(-double(rows) / G)) + double(rows) / (16 * nt);
   double best = 0.0;

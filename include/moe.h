@@ -414,9 +414,11 @@ moe_status moe_combine(moe_layer_t layer, const uint16_t* y, const int32_t* inv,
  *     the status word; a routing-only handle is enough. Its hidden and ffn
  *     are not used: the sizes are arguments. The current device must be the
  *     handle's, else MOE_ERR_INVALID_ARG;
- *   - offsets [E+2] are the groups' rows as moe_permute, moe_ep_plan or
- *     moe_ep_dispatch write them: group g is rows [offsets[g], offsets[g+1]),
- *     empty groups are allowed, group E must be empty when S = 0. Rows before
+ *   - offsets [E+2] are the groups' rows as moe_permute or moe_ep_plan write
+ *     them (moe_ep_dispatch writes offsets of the same form, for the FP8 rows
+ *     that it moves; it moves no others): group g is rows
+ *     [offsets[g], offsets[g+1]), empty groups are allowed, group E must be
+ *     empty when S = 0. Rows before
  *     offsets[0] and from offsets[E+1] to `rows` belong to no group: what
  *     they hold is not used and their outputs are left as they were. Offsets
  *     that start below 0, decrease or end beyond `rows` set
@@ -469,8 +471,10 @@ moe_status moe_grouped_mm_wgrad(moe_layer_t layer, moe_dtype type, const void* d
  *   h[r, j] = silu(gate[r, j]) * up[r, j],  silu(g) = g / (1 + exp(-g))
  * over the rows of all groups (offsets as above; NULL: all `rows` rows).
  *   type   MOE_BF16, MOE_F16 or MOE_F32: gate, up [rows][ld] and h; fp32
- *          arithmetic; any stride, aligned to the element. h may be gate or
- *          up itself (same pointer and stride). */
+ *          arithmetic, in an order in which nothing leaves fp32's range
+ *          unless the result does (a gate of -88 and an up of 1e38 give -53);
+ *          any stride, aligned to the element. h may be gate or up itself
+ *          (same pointer and stride). */
 moe_status moe_swiglu(moe_layer_t layer, moe_dtype type, const void* gate, long long ldg, const void* up,
                       long long ldu, const int32_t* offsets, int rows, int f, void* h, long long ldh, void* stream);
 /* Gradient of moe_swiglu, with s = 1 / (1 + exp(-gate)):
