@@ -429,6 +429,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
         }
       }
       s_issued = it;
+      // the MMAs' arrivals on this CTA's barriers, which come from the leading
+      // CTA, are all in before it may end
+      for (uint32_t j = it > STAGES ? it - STAGES : 0; ok && j < it; ++j)
+        ok = mbar_wait_stage<true>(&empty_bar[j % STAGES], (j / STAGES) & 1u, s_abort, p.status, p.wait_ns);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -465,7 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(BR, PROMOTE)
             // atoms (2048 bytes) of an MN-major box (address field in 16 bytes)
             if (MODE != MOE_MM_WGRAD || k * 16 < left)
               mma_f16_pair(d, ad + uint64_t(k * (A_MN ? 128 : 2)), bd + uint64_t(k * (B_MN ? 128 : 2)), idesc,
-                         (part | k) ? 1u : 0u);
+                           (part | k) ? 1u : 0u);
           tc_commit_pair(&empty_bar[s]);
           ++it;
           ++part;
