@@ -27,11 +27,12 @@
 // through its own ring of two TMA boxes (64 rows x 128 bytes = 256 codes,
 // 128-byte swizzle: lane (g, t) reads word t of a chunk of row g without bank
 // conflicts), so no warp waits for another until a unit's partial sums meet in
-// shared memory, added in warp order. The warps of a CTA split the contraction 4, 2 or 1 ways and the
-// columns by the rest (see launch_w4). Measured and dropped: 16 warps per SM
-// with 128-code stages (465 against 418 us) and 128 rows per warp (500 against
-// 439), both for their 64-byte boxes; 24 warps of 80 registers (no gain at 64
-// tokens, 102 against 86 us for the down projection).
+// shared memory, added in warp order. The warps of a CTA split the contraction
+// 4, 2 or 1 ways and the columns by the rest (see launch_w4). Measured and
+// dropped: 16 warps per SM with 128-code stages (465 against 418 us) and 128
+// rows per warp (500 against 439), both for their 64-byte boxes; 24 warps of
+// 80 registers (no gain at 64 tokens, 102 against 86 us for the down
+// projection).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
